@@ -86,6 +86,25 @@ def ffn_desc(m, d_model, d_ff, act="gelu_tanh", dtype="bf16"):
     return dlf_ffn_desc(m, d_model, d_ff, DTYPES.get(dtype, dtype), ACTS.get(act, act))
 
 
+class dlf_kv_cache_desc(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int), ("k_scale", ctypes.c_float),
+                ("v_scale", ctypes.c_float)]
+
+
+def kv_cache_desc(pages, kv_heads, page_size, head_dim, dtype="bf16", k_scale=1.0, v_scale=1.0):
+    return dlf_kv_cache_desc(pages, kv_heads, page_size, head_dim, DTYPES.get(dtype, dtype), k_scale, v_scale)
+
+
+class dlf_page_plan_desc(ctypes.Structure):
+    _fields_ = [("requests", ctypes.c_int32), ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("token_cap", ctypes.c_int32), ("free_cap", ctypes.c_int32)]
+
+
+def page_plan_desc(requests, page_size, max_pages, token_cap, free_cap):
+    return dlf_page_plan_desc(requests, page_size, max_pages, token_cap, free_cap)
+
+
 class dlf_graph_node(ctypes.Structure):
     _fields_ = [("op", ctypes.c_int32), ("n_inputs", ctypes.c_int32), ("inputs", ctypes.c_int32 * 2),
                 ("dtype", ctypes.c_int32), ("flags", ctypes.c_uint32), ("rank", ctypes.c_int32),
@@ -121,6 +140,8 @@ _SIGS = {
     "dlf_ffn_fused_ws": [ctypes.POINTER(dlf_ffn_desc), _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t,
                          _vp],
     "dlf_ffn_fused_noalloc": [ctypes.POINTER(dlf_ffn_desc), _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp],
+    "dlf_page_plan": [ctypes.POINTER(dlf_page_plan_desc)] + [_vp] * 11,
+    "dlf_paged_store": [ctypes.POINTER(dlf_kv_cache_desc), _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp],
     "dlf_clock_probe": [ctypes.c_int32, ctypes.c_int32, _vp, _vp],
     "dlf_fusion_plan": [ctypes.POINTER(dlf_graph_node), ctypes.c_int32, ctypes.c_double, ctypes.c_double,
                         ctypes.POINTER(dlf_fusion_group), ctypes.c_int32, ctypes.POINTER(ctypes.c_int32)],
@@ -318,6 +339,40 @@ def dlf_ffn_fused_noalloc(desc, x, w1_packed, b1, w2_packed, b2, residual, y, st
     device scratch (see include/dlfusion.h)."""
     _check(_lib.dlf_ffn_fused_noalloc(ctypes.byref(desc), _dev(x), _dev(w1_packed), _dev(b1), _dev(w2_packed),
                                       _dev(b2), _dev(residual), _dev(y), _stream(stream)), "dlf_ffn_fused_noalloc")
+
+
+def _rows(t, rank):
+    """(device pointer, elements between rows) of a torch tensor whose dimensions after the first
+    are contiguous: [rows][...] with `rank` dimensions; the first may have any stride."""
+    shape, strides = t.shape, t.stride()
+    if len(shape) != rank:
+        raise ValueError(f"a tensor of {rank} dimensions is needed, got {len(shape)}")
+    width = 1
+    for n, st in zip(reversed(shape[1:]), reversed(strides[1:])):
+        if n != 1 and st != width:
+            raise ValueError("the dimensions after the first must be contiguous")
+        width *= n
+    return t.data_ptr(), strides[0] if shape[0] > 1 else width
+
+
+def dlf_page_plan(desc, cached, fresh, free_pages, free_head, block_table, starts, lens, slots, rows, counts,
+                  stream=None):
+    """Block tables and slot maps of a step, from the requests' lengths (see include/dlfusion.h)."""
+    _check(_lib.dlf_page_plan(ctypes.byref(desc), _dev(cached), _dev(fresh), _dev(free_pages), _dev(free_head),
+                              _dev(block_table), _dev(starts), _dev(lens), _dev(slots), _dev(rows), _dev(counts),
+                              _stream(stream)), "dlf_page_plan")
+
+
+def dlf_paged_store(cache, k, v, slots, k_cache, v_cache, stream=None):
+    """New keys and values [tokens][kv_heads][head_dim] into the cache's slots; the rows of k and v
+    may be any distance apart (column blocks of a fused QKV product)."""
+    kp, ks = _rows(k, 3)
+    vp, vs = _rows(v, 3)
+    tokens = k.shape[0]
+    if k.shape != v.shape or tuple(k.shape[1:]) != (cache.kv_heads, cache.head_dim) or slots.shape[0] != tokens:
+        raise ValueError("k and v must be [tokens][kv_heads][head_dim], slots [tokens]")
+    _check(_lib.dlf_paged_store(ctypes.byref(cache), tokens, kp, ks, vp, vs, _dev(slots), _dev(k_cache), _dev(v_cache),
+                                _stream(stream)), "dlf_paged_store")
 
 
 def dlf_clock_probe(workgroups, iters, stamps, stream=None):

@@ -164,6 +164,36 @@ struct FfnArgs {
 int ffn_parts(int64_t M, int D, int F);
 hipError_t launch_ffn(const FfnArgs& args, int act, hipStream_t stream);
 
+// Page plan: block tables and slot maps from request lengths (dlf_page_plan).
+struct PagePlanArgs {
+    const int32_t* cached;      // [requests]
+    const int32_t* fresh;       // [requests]
+    const int32_t* free_pages;  // [free_cap]
+    const int32_t* free_head;   // nullable (= 0)
+    int32_t* table;             // [requests][max_pages]
+    int32_t* starts;            // [requests + 1]
+    int32_t* lens;              // [requests]
+    int64_t* slots;             // [token_cap]
+    int32_t* rows;              // [token_cap] or nullptr
+    int32_t* counts;            // [4]
+    int requests, page_size, max_pages, token_cap, free_cap;
+};
+hipError_t launch_page_plan(const PagePlanArgs& args, hipStream_t stream);
+
+// New keys and values into the paged cache's slots (dlf_paged_store).
+struct PagedStoreArgs {
+    const uint16_t* src[2];     // k, v: [tokens][kv_heads][head_dim], rows stride[] apart
+    void* cache[2];             // [pages][kv_heads][page_size][head_dim]
+    const int64_t* slots;       // [tokens]
+    int64_t stride[2];
+    float inv_scale[2];         // fp8 cache
+    int64_t tokens;
+    int64_t slot_count;         // pages * page_size (< 2^31)
+    int kv_heads, head_dim, page_size;
+    bool fp8;
+};
+hipError_t launch_paged_store(const PagedStoreArgs& args, hipStream_t stream);
+
 // Shader-clock probe: workgroups x 4 waves of back-to-back bf16 MFMAs; stamps[4 b + 0..3] =
 // s_memtime before / after, s_memrealtime before / after, for workgroup b.
 hipError_t launch_clock_probe(int workgroups, int iters, uint64_t* stamps, hipStream_t stream);

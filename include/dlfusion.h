@@ -383,6 +383,87 @@ dlf_status dlf_ffn_fused_noalloc(const dlf_ffn_desc *d, const void *x, const voi
                                  const void *residual, void *y, void *stream);
 
 /* ---------------------------------------------------------------------- */
+/* Decoding over a paged key-value cache                                    */
+/* ---------------------------------------------------------------------- */
+
+/* One layer's key or value cache.  Its memory is a pool of `pages` pages,
+ *     cache[page][kv_head][slot in page][head_dim],
+ * so that the tokens of one page and head are one contiguous run (4 KB at 16
+ * tokens of 128 bf16 values) and a head's attention reads nothing else.
+ * Keys and values have a pool each, of the same shape.  Token t of a request
+ * lives on page block_table[request][t / page_size]; its slot number is
+ * page * page_size + t % page_size.
+ * dtype BF16, or FP8_E4M3: codes of value / scale with the static scales
+ * k_scale and v_scale, as the fp8 GEMM's output has them.  The scales of a
+ * BF16 cache are not used. */
+typedef struct {
+    int32_t pages;              /* pages of the pool, >= 1; pages * page_size < 2^31 */
+    int32_t kv_heads;
+    int32_t page_size;          /* tokens a page: a multiple of 16, at most 32768 */
+    int32_t head_dim;           /* 64, 128 or 256 */
+    dlf_dtype dtype;            /* BF16 or FP8_E4M3 */
+    float k_scale, v_scale;     /* FP8_E4M3: finite and > 0 */
+} dlf_kv_cache_desc;
+
+/* Sizes of a page plan. */
+typedef struct {
+    int32_t requests;           /* 0 .. 65536 */
+    int32_t page_size;          /* tokens a page, >= 1 */
+    int32_t max_pages;          /* columns of block_table, >= 1; max_pages * page_size < 2^31 */
+    int32_t token_cap;          /* entries of slots and rows */
+    int32_t free_cap;           /* entries of free_pages */
+} dlf_page_plan_desc;
+
+/* Block tables and slot maps of a step, built on the device from the requests'
+ * lengths (no host synchronisation, so a step may be captured in a graph).
+ * Request r has cached[r] tokens in the cache and brings fresh[r] more; with
+ * cap = max_pages * page_size and negative counts read as 0,
+ *     lens[r] = min(cached[r] + fresh[r], cap)
+ *     need[r] = ceil(lens[r] / page_size) - ceil(min(cached[r], cap) / page_size)
+ * and the need[r] table entries after the cached ones are filled from
+ * free_pages, in the order of the requests from index free_head on.  Every
+ * other table entry is left as it is.  A page that the free list does not
+ * have is entered as -1.  The fresh tokens are numbered request by request:
+ *     starts[r]  the number of fresh tokens before request r (starts[requests]: all;
+ *                held at 2^31 - 1)
+ *     rows[t]    the request of fresh token t, -1 past the last
+ *     slots[t]   where its key and value go, -1 where there is no page for it
+ *                and past the last
+ *     counts     fresh tokens (held at 2^31 - 1), the free list's head after the step
+ *                (the next call's free_head), the longest lens, pages that were missing
+ *   cached, fresh  device [requests] int32
+ *   free_pages     device [free_cap] int32, may be NULL when free_cap == 0
+ *   free_head      device int32 or NULL (= 0); read as 0 where negative
+ *   block_table    device [requests][max_pages] int32, in and out
+ *   starts         device [requests + 1] int32
+ *   lens           device [requests] int32
+ *   slots, rows    device [token_cap] int64 and int32; rows may be NULL
+ *   counts         device [4] int32
+ * Tokens past token_cap get no entry (counts[0] tells).  int32 arrays are
+ * 4-byte aligned, slots 8-byte.  ALIAS: an output overlaps an input or another
+ * output.  UNSUPPORTED: more than 65536 requests, or max_pages * page_size >=
+ * 2^31. */
+dlf_status dlf_page_plan(const dlf_page_plan_desc *d, const int32_t *cached, const int32_t *fresh,
+                         const int32_t *free_pages, const int32_t *free_head, int32_t *block_table,
+                         int32_t *starts, int32_t *lens, int64_t *slots, int32_t *rows,
+                         int32_t *counts, void *stream);
+
+/* Keys and values of new tokens into the cache's slots:
+ *     BF16:      cache[slot] = k
+ *     FP8_E4M3:  cache[slot] = Q( fp32(k * fp32(1 / k_scale)) ), values likewise
+ * with the quantiser Q of the fp8 GEMM, except that a NaN stays a NaN.
+ *   k, v      device bf16 [tokens][kv_heads][head_dim], rows k_stride / v_stride
+ *             elements apart (a multiple of 8; >= kv_heads * head_dim): column
+ *             blocks of a fused QKV product need no copy
+ *   slots     device [tokens] int64; a slot outside the cache (-1) is skipped.
+ *             Two tokens with one slot: either is stored
+ *   k_cache, v_cache  device, laid out as in dlf_kv_cache_desc
+ * ALIAS: a cache overlaps an input or the other cache. */
+dlf_status dlf_paged_store(const dlf_kv_cache_desc *c, int64_t tokens, const void *k, int64_t k_stride,
+                           const void *v, int64_t v_stride, const int64_t *slots, void *k_cache,
+                           void *v_cache, void *stream);
+
+/* ---------------------------------------------------------------------- */
 /* Host fusion pass: which chains of a graph become one fused launch        */
 /* ---------------------------------------------------------------------- */
 

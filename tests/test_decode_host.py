@@ -1,0 +1,118 @@
+"""CPU tests of the decode operators' argument checks.  Nothing here launches a kernel: every call
+is rejected, or is a zero-size no-op, before any HIP call."""
+import ctypes
+
+import pytest
+
+dlf = pytest.importorskip("dl_fusion_amd", reason="libdlfusion.so not built")
+from test_host_lib import fake_pointers  # noqa: E402
+
+INVALID, UNSUPPORTED, ALIAS = dlf.DLF_ERR_INVALID_ARG, dlf.DLF_ERR_UNSUPPORTED, dlf.DLF_ERR_ALIAS
+MB = 1 << 20
+
+
+def addr(i, off=0):
+    """Fake device addresses, 64 GB apart, never dereferenced."""
+    return (i + 1) * (64 << 30) + off
+
+
+def ref(d):
+    return None if d is None else ctypes.byref(d)
+
+
+# ---------------------------------------------------------------------------
+# Page plan
+# ---------------------------------------------------------------------------
+PLAN_PTRS = ("cached", "fresh", "free_pages", "free_head", "block_table", "starts", "lens", "slots", "rows", "counts")
+
+
+def call_plan(desc=(8, 16, 4, 32, 64), **ptrs):
+    p = {n: addr(i) for i, n in enumerate(PLAN_PTRS)}
+    p.update(ptrs)
+    d = None if desc is None else dlf.page_plan_desc(*desc)
+    return dlf.raw().dlf_page_plan(ref(d), *[p[n] for n in PLAN_PTRS], None)
+
+
+@fake_pointers
+def test_page_plan_refusals():
+    assert call_plan(None) == INVALID
+    for bad in [(-1, 16, 4, 32, 64), (8, 0, 4, 32, 64), (8, 16, 0, 32, 64), (8, 16, 4, -1, 64), (8, 16, 4, 32, -1),
+                (8, -16, 4, 32, 64)]:
+        assert call_plan(bad) == INVALID, bad
+    assert call_plan((65537, 16, 4, 32, 64)) == UNSUPPORTED
+    assert call_plan((8, 1 << 16, 1 << 15, 32, 64)) == UNSUPPORTED
+    for n in ("cached", "fresh", "free_pages", "block_table", "starts", "lens", "slots", "counts"):
+        assert call_plan(**{n: None}) == INVALID, n
+    for n in PLAN_PTRS:
+        assert call_plan(**{n: addr(40, 2)}) == INVALID, n
+    assert call_plan(slots=addr(40, 4)) == INVALID
+    assert "aligned" in dlf.dlf_last_error()
+    # an output over an input, two outputs over each other, an output over the free list's head
+    assert call_plan(lens=addr(0, 28)) == ALIAS
+    assert call_plan(rows=addr(7, 8 * 32 - 4)) == ALIAS
+    assert call_plan(counts=addr(3)) == ALIAS
+
+
+# ---------------------------------------------------------------------------
+# Store
+# ---------------------------------------------------------------------------
+def cache(**kw):
+    args = dict(pages=8, kv_heads=2, page_size=16, head_dim=64, dtype="bf16", k_scale=1.0, v_scale=1.0)
+    args.update(kw)
+    return dlf.kv_cache_desc(**args)
+
+
+BAD_CACHES = [
+    (dict(dtype=7), INVALID), (dict(dtype="f32"), UNSUPPORTED), (dict(pages=0), INVALID), (dict(pages=-3), INVALID),
+    (dict(kv_heads=0), INVALID), (dict(page_size=0), INVALID), (dict(head_dim=0), INVALID),
+    (dict(head_dim=96), UNSUPPORTED), (dict(head_dim=512), UNSUPPORTED), (dict(page_size=8), UNSUPPORTED),
+    (dict(page_size=24), UNSUPPORTED), (dict(page_size=65536), UNSUPPORTED), (dict(kv_heads=5000), UNSUPPORTED),
+    (dict(pages=1 << 27), UNSUPPORTED), (dict(dtype="fp8", k_scale=0.0), INVALID),
+    (dict(dtype="fp8", v_scale=-1.0), INVALID), (dict(dtype="fp8", k_scale=float("nan")), INVALID),
+    (dict(dtype="fp8", v_scale=float("inf")), INVALID), (dict(dtype="fp8", k_scale=1e-45), INVALID),
+]
+
+
+def call_store(c, tokens=4, ks=128, vs=128, k=addr(0), v=addr(1), slots=addr(2), kc=addr(3), vc=addr(4)):
+    return dlf.raw().dlf_paged_store(ref(c), tokens, k, ks, v, vs, slots, kc, vc, None)
+
+
+@fake_pointers
+@pytest.mark.parametrize("kw,status", BAD_CACHES)
+def test_store_refuses_bad_caches(kw, status):
+    assert call_store(cache(**kw)) == status
+
+
+@fake_pointers
+def test_store_refusals():
+    c = cache()
+    assert call_store(None) == INVALID
+    assert call_store(c, tokens=-1) == INVALID
+    assert call_store(c, tokens=(1 << 30) + 1) == UNSUPPORTED
+    assert call_store(c, tokens=0, k=None, kc=None) == dlf.DLF_OK
+    assert call_store(c, ks=120) == INVALID
+    assert call_store(c, vs=132) == UNSUPPORTED
+    assert call_store(c, vs=(1 << 31) + 8) == UNSUPPORTED
+    for n in ("k", "v", "slots", "kc", "vc"):
+        assert call_store(c, **{n: None}) == INVALID, n
+    for n in ("k", "v", "kc", "vc"):
+        assert call_store(c, **{n: addr(40, 8)}) == INVALID, n
+    assert call_store(c, slots=addr(40, 4)) == INVALID
+    size = 8 * 2 * 16 * 64 * 2
+    assert call_store(c, vc=addr(3, size - 16)) == ALIAS
+    assert call_store(c, kc=addr(0, (3 * 128 + 128) * 2 - 16)) == ALIAS
+    # with rows 256 apart the last row ends later
+    assert call_store(c, ks=256, kc=addr(0, (3 * 256 + 128) * 2 - 16)) == ALIAS
+    assert call_store(c, slots=addr(4, 64)) == ALIAS
+
+
+def test_store_binding_checks_shapes():
+    torch = pytest.importorskip("torch")
+    c = cache()
+    k = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
+    slots = torch.zeros(4, dtype=torch.int64)
+    for bad in (k[:, :, ::2], k[:, :1], k.view(4, 128), k.transpose(0, 1)):
+        with pytest.raises(ValueError):
+            dlf.dlf_paged_store(c, bad, bad, slots, k, k, stream=0)
+    with pytest.raises(ValueError):
+        dlf.dlf_paged_store(c, k, k, slots[:3], k, k, stream=0)
