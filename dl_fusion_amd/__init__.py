@@ -105,6 +105,17 @@ def page_plan_desc(requests, page_size, max_pages, token_cap, free_cap):
     return dlf_page_plan_desc(requests, page_size, max_pages, token_cap, free_cap)
 
 
+class dlf_paged_attn_desc(ctypes.Structure):
+    _fields_ = [("cache", dlf_kv_cache_desc), ("requests", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("window", ctypes.c_int32), ("max_len", ctypes.c_int32),
+                ("q_stride", ctypes.c_int64), ("softmax_scale", ctypes.c_float)]
+
+
+def paged_attn_desc(cache, requests, heads, max_pages, softmax_scale, window=0, max_len=0, q_stride=None):
+    return dlf_paged_attn_desc(cache, requests, heads, max_pages, window, max_len,
+                               heads * cache.head_dim if q_stride is None else q_stride, softmax_scale)
+
+
 class dlf_graph_node(ctypes.Structure):
     _fields_ = [("op", ctypes.c_int32), ("n_inputs", ctypes.c_int32), ("inputs", ctypes.c_int32 * 2),
                 ("dtype", ctypes.c_int32), ("flags", ctypes.c_uint32), ("rank", ctypes.c_int32),
@@ -142,6 +153,8 @@ _SIGS = {
     "dlf_ffn_fused_noalloc": [ctypes.POINTER(dlf_ffn_desc), _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp],
     "dlf_page_plan": [ctypes.POINTER(dlf_page_plan_desc)] + [_vp] * 11,
     "dlf_paged_store": [ctypes.POINTER(dlf_kv_cache_desc), _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp],
+    "dlf_paged_attention_workspace_bytes": [ctypes.POINTER(dlf_paged_attn_desc), ctypes.POINTER(ctypes.c_size_t)],
+    "dlf_paged_attention": [ctypes.POINTER(dlf_paged_attn_desc)] + [_vp] * 8 + [ctypes.c_size_t, _vp],
     "dlf_clock_probe": [ctypes.c_int32, ctypes.c_int32, _vp, _vp],
     "dlf_fusion_plan": [ctypes.POINTER(dlf_graph_node), ctypes.c_int32, ctypes.c_double, ctypes.c_double,
                         ctypes.POINTER(dlf_fusion_group), ctypes.c_int32, ctypes.POINTER(ctypes.c_int32)],
@@ -373,6 +386,29 @@ def dlf_paged_store(cache, k, v, slots, k_cache, v_cache, stream=None):
         raise ValueError("k and v must be [tokens][kv_heads][head_dim], slots [tokens]")
     _check(_lib.dlf_paged_store(ctypes.byref(cache), tokens, kp, ks, vp, vs, _dev(slots), _dev(k_cache), _dev(v_cache),
                                 _stream(stream)), "dlf_paged_store")
+
+
+def dlf_paged_attention_workspace_bytes(desc):
+    n = ctypes.c_size_t(0)
+    _check(_lib.dlf_paged_attention_workspace_bytes(ctypes.byref(desc), ctypes.byref(n)),
+           "dlf_paged_attention_workspace_bytes")
+    return n.value
+
+
+def dlf_paged_attention(desc, q, k_cache, v_cache, block_table, lens, out, lse, workspace, workspace_bytes,
+                        stream=None):
+    """Attention of one new token per request over the paged cache.  q is [requests][heads][head_dim]
+    with its requests desc.q_stride elements apart (a column block of a fused QKV product)."""
+    if isinstance(q, int):
+        qp = q
+    else:
+        qp, qs = _rows(q, 3)
+        if tuple(q.shape) != (desc.requests, desc.heads, desc.cache.head_dim) or (q.shape[0] > 1 and
+                                                                                  qs != desc.q_stride):
+            raise ValueError("q must be [requests][heads][head_dim], its requests q_stride elements apart")
+    _check(_lib.dlf_paged_attention(ctypes.byref(desc), qp, _dev(k_cache), _dev(v_cache), _dev(block_table),
+                                    _dev(lens), _dev(out), _dev(lse), _dev(workspace), int(workspace_bytes),
+                                    _stream(stream)), "dlf_paged_attention")
 
 
 def dlf_clock_probe(workgroups, iters, stamps, stream=None):

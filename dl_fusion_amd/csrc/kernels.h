@@ -194,6 +194,24 @@ struct PagedStoreArgs {
 };
 hipError_t launch_paged_store(const PagedStoreArgs& args, hipStream_t stream);
 
+// Attention of one new token per request over the paged cache (dlf_paged_attention).
+struct PagedAttnArgs {
+    const uint16_t* q;          // [requests][heads][head_dim], requests q_stride apart
+    const uint8_t* k;           // [pages][kv_heads][page_size][head_dim]
+    const uint8_t* v;
+    const int32_t* table;       // [requests][max_pages]
+    const int32_t* lens;        // [requests]
+    uint16_t* out;              // [requests][heads][head_dim]
+    float* lse;                 // [requests][heads] or nullptr
+    int64_t q_stride;
+    int requests, heads, kv_heads, page_size, pages, max_pages, window;
+    int group;                  // heads / kv_heads
+    int head_tiles;             // ceil(group / 16)
+    float score_scale;          // softmax_scale * k_scale * log2(e)
+    float v_scale;
+};
+hipError_t launch_paged_attention(const PagedAttnArgs& args, int head_dim, bool fp8, hipStream_t stream);
+
 // Shader-clock probe: workgroups x 4 waves of back-to-back bf16 MFMAs; stamps[4 b + 0..3] =
 // s_memtime before / after, s_memrealtime before / after, for workgroup b.
 hipError_t launch_clock_probe(int workgroups, int iters, uint64_t* stamps, hipStream_t stream);

@@ -1,4 +1,4 @@
-// C ABI of the paged key-value cache: the page plan and the store.  Every check happens before
+// C ABI of the paged key-value cache: the page plan, the store and the attention that reads it.  Every check happens before
 // the first HIP call.
 #include <hip/hip_runtime.h>
 
@@ -124,5 +124,92 @@ extern "C" dlf_status dlf_paged_store(const dlf_kv_cache_desc* c, int64_t tokens
     a.page_size = c->page_size;
     const hipError_t e = dlf::launch_paged_store(a, static_cast<hipStream_t>(stream));
     if (e != hipSuccess) return fail(DLF_ERR_HIP, "dlf_paged_store: %s", hipGetErrorString(e));
+    return ok();
+}
+
+namespace {
+
+// the descriptor's checks; fills the kernel's sizes
+dlf_status check_attn_desc(const dlf_paged_attn_desc* d, dlf::PagedAttnArgs* a) {
+    if (!d) return fail(DLF_ERR_INVALID_ARG, "attention descriptor is NULL");
+    const dlf_kv_cache_desc* c = &d->cache;
+    const dlf_status st = check_cache(c);
+    if (st != DLF_OK) return st;
+    if (d->requests < 0 || d->window < 0 || d->max_len < 0)
+        return fail(DLF_ERR_INVALID_ARG, "requests, window and max_len must not be negative");
+    if (d->max_pages < 1) return fail(DLF_ERR_INVALID_ARG, "max_pages must be positive");
+    if (d->heads < 1 || d->heads % c->kv_heads != 0)
+        return fail(DLF_ERR_INVALID_ARG, "heads must be a positive multiple of kv_heads");
+    if (!std::isfinite(d->softmax_scale)) return fail(DLF_ERR_INVALID_ARG, "softmax_scale must be finite");
+    if (static_cast<int64_t>(d->max_pages) * c->page_size >= (int64_t(1) << 31))
+        return fail(DLF_ERR_UNSUPPORTED, "max_pages * page_size must stay below 2^31");
+    const int group = d->heads / c->kv_heads;
+    if (group > 256) return fail(DLF_ERR_UNSUPPORTED, "more than 256 query heads to a kv head");
+    if (d->requests > 65536) return fail(DLF_ERR_UNSUPPORTED, "more than 65536 requests");
+    if (d->q_stride < static_cast<int64_t>(d->heads) * c->head_dim)
+        return fail(DLF_ERR_INVALID_ARG, "q_stride is below heads * head_dim");
+    if (d->q_stride % 8 != 0 || d->q_stride > kMaxStride)
+        return fail(DLF_ERR_UNSUPPORTED, "q_stride must be a multiple of 8, at most 2^31");
+    *a = dlf::PagedAttnArgs{};
+    a->q_stride = d->q_stride;
+    a->requests = d->requests;
+    a->heads = d->heads;
+    a->kv_heads = c->kv_heads;
+    a->page_size = c->page_size;
+    a->pages = c->pages;
+    a->max_pages = d->max_pages;
+    a->window = d->window;
+    a->group = group;
+    a->head_tiles = (group + 15) / 16;
+    if (static_cast<int64_t>(d->requests) * c->kv_heads * a->head_tiles >= (int64_t(1) << 31))
+        return fail(DLF_ERR_UNSUPPORTED, "requests * kv_heads must stay below 2^31");
+    const bool fp8 = c->dtype == DLF_FP8_E4M3;
+    a->score_scale = static_cast<float>(static_cast<double>(d->softmax_scale) * (fp8 ? c->k_scale : 1.0f) *
+                                        1.4426950408889634074);
+    a->v_scale = fp8 ? c->v_scale : 1.0f;
+    return ok();
+}
+
+}  // namespace
+
+extern "C" dlf_status dlf_paged_attention_workspace_bytes(const dlf_paged_attn_desc* d, size_t* bytes) {
+    if (!bytes) return fail(DLF_ERR_INVALID_ARG, "bytes is NULL");
+    *bytes = 0;
+    dlf::PagedAttnArgs a;
+    return check_attn_desc(d, &a);
+}
+
+extern "C" dlf_status dlf_paged_attention(const dlf_paged_attn_desc* d, const void* q, const void* k_cache,
+                                          const void* v_cache, const int32_t* block_table, const int32_t* lens,
+                                          void* out, float* lse, void* workspace, size_t workspace_bytes,
+                                          void* stream) {
+    dlf::PagedAttnArgs a;
+    const dlf_status st = check_attn_desc(d, &a);
+    if (st != DLF_OK || d->requests == 0) return st;
+    if (!q || !k_cache || !v_cache || !block_table || !lens || !out)
+        return fail(DLF_ERR_INVALID_ARG, "q, the caches, block_table, lens and out must be non-NULL");
+    if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
+        !aligned(block_table, 4) || !aligned(lens, 4) || !aligned(lse, 4))
+        return fail(DLF_ERR_INVALID_ARG, "device pointers must be 16-byte aligned (int32 and fp32 arrays 4)");
+    const size_t r = static_cast<size_t>(d->requests), rows = r * static_cast<size_t>(d->heads);
+    const size_t width = static_cast<size_t>(d->cache.head_dim);
+    const dlf::Span qs{q, rows_bytes(d->requests, d->q_stride, static_cast<int64_t>(d->heads) * d->cache.head_dim, 2)};
+    const dlf::Span ks{k_cache, cache_bytes(&d->cache)}, vs{v_cache, cache_bytes(&d->cache)};
+    const dlf::Span ts{block_table, r * static_cast<size_t>(d->max_pages) * 4}, ls{lens, r * 4};
+    const dlf::Span os{out, rows * width * 2}, es{lse, rows * 4};
+    if (any_overlap({os, es}, {qs, ks, vs, ts, ls}))
+        return fail(DLF_ERR_ALIAS, "an output overlaps an input or the other output");
+    (void)workspace;
+    (void)workspace_bytes;
+    a.q = static_cast<const uint16_t*>(q);
+    a.k = static_cast<const uint8_t*>(k_cache);
+    a.v = static_cast<const uint8_t*>(v_cache);
+    a.table = block_table;
+    a.lens = lens;
+    a.out = static_cast<uint16_t*>(out);
+    a.lse = lse;
+    const hipError_t e = dlf::launch_paged_attention(a, d->cache.head_dim, d->cache.dtype == DLF_FP8_E4M3,
+                                                     static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return fail(DLF_ERR_HIP, "dlf_paged_attention: %s", hipGetErrorString(e));
     return ok();
 }

@@ -463,6 +463,54 @@ dlf_status dlf_paged_store(const dlf_kv_cache_desc *c, int64_t tokens, const voi
                            const void *v, int64_t v_stride, const int64_t *slots, void *k_cache,
                            void *v_cache, void *stream);
 
+/* Attention of one new token per request over the paged cache. */
+typedef struct {
+    dlf_kv_cache_desc cache;
+    int32_t requests;
+    int32_t heads;              /* query heads, a multiple of cache.kv_heads: head h reads
+                                 * kv head h / (heads / kv_heads) */
+    int32_t max_pages;          /* columns of block_table */
+    int32_t window;             /* 0, or the last tokens that a request attends to */
+    int32_t max_len;            /* 0, or an upper bound of lens known to the host: chooses the
+                                 * launch, never the result */
+    int64_t q_stride;           /* elements between two requests' queries, a multiple of 8 */
+    float softmax_scale;
+} dlf_paged_attn_desc;
+
+/* Bytes of device workspace dlf_paged_attention needs for d, written to
+ * *bytes.  The descriptor checks and statuses of dlf_paged_attention; bytes
+ * NULL: DLF_ERR_INVALID_ARG.  Host only. */
+dlf_status dlf_paged_attention_workspace_bytes(const dlf_paged_attn_desc *d, size_t *bytes);
+
+/* For request r and head h, over the tokens j in [max(0, len - window), len),
+ * len = lens[r] (read as 0 where negative, as max_pages * page_size where
+ * beyond):
+ *     s_j = softmax_scale * q . k_j
+ *     out = sum_j exp(s_j - lse) v_j,   lse = ln sum_j exp(s_j)
+ * The keys and values of an FP8_E4M3 cache are code * scale.  A token whose
+ * table entry is not a page of the pool is left out; a request with no token
+ * left has out = 0 and lse = -inf.  Cache slots past a request's length are
+ * never used, whatever they hold.  Scores, statistics and sums are fp32; the
+ * probabilities enter the second product as a sum of two bf16 values (2^-17
+ * relative), and out is rounded once.  Keys or values in range that are not
+ * finite give outputs that are not finite.
+ *   q            device bf16 [requests][heads][head_dim], requests q_stride apart
+ *   k_cache, v_cache  device, laid out as in dlf_kv_cache_desc
+ *   block_table  device [requests][max_pages] int32
+ *   lens         device [requests] int32, the new token's key included
+ *   out          device bf16 [requests][heads][head_dim], contiguous
+ *   lse          device fp32 [requests][heads] or NULL
+ *   workspace    device, 16-byte aligned, at least
+ *                dlf_paged_attention_workspace_bytes(d) bytes, overlapping no
+ *                operand; may be NULL where that size is 0.  Scratch: calls
+ *                that share one on overlapping streams race
+ * UNSUPPORTED: a head_dim, page_size or cache dtype not named above, more
+ * than 256 query heads to a kv head, q_stride % 8 != 0. */
+dlf_status dlf_paged_attention(const dlf_paged_attn_desc *d, const void *q, const void *k_cache,
+                               const void *v_cache, const int32_t *block_table, const int32_t *lens,
+                               void *out, float *lse, void *workspace, size_t workspace_bytes,
+                               void *stream);
+
 /* ---------------------------------------------------------------------- */
 /* Host fusion pass: which chains of a graph become one fused launch        */
 /* ---------------------------------------------------------------------- */

@@ -116,3 +116,83 @@ def test_store_binding_checks_shapes():
             dlf.dlf_paged_store(c, bad, bad, slots, k, k, stream=0)
     with pytest.raises(ValueError):
         dlf.dlf_paged_store(c, k, k, slots[:3], k, k, stream=0)
+
+
+# ---------------------------------------------------------------------------
+# Attention
+# ---------------------------------------------------------------------------
+ATTN_PTRS = ("q", "k_cache", "v_cache", "block_table", "lens", "out", "lse", "workspace")
+
+
+def attn(c=None, **kw):
+    args = dict(requests=4, heads=8, max_pages=4, softmax_scale=0.125)
+    args.update(kw)
+    return dlf.paged_attn_desc(cache() if c is None else c, **args)
+
+
+def call_attn(d, ws_bytes=1 << 30, **ptrs):
+    p = {n: addr(i) for i, n in enumerate(ATTN_PTRS)}
+    p.update(ptrs)
+    return dlf.raw().dlf_paged_attention(ref(d), *[p[n] for n in ATTN_PTRS], ws_bytes, None)
+
+
+def attn_bytes(d):
+    n = ctypes.c_size_t(123)
+    st = dlf.raw().dlf_paged_attention_workspace_bytes(ref(d), ctypes.byref(n))
+    return st, n.value
+
+
+BAD_ATTN = [
+    (dict(requests=-1), INVALID), (dict(window=-1), INVALID), (dict(max_len=-1), INVALID), (dict(max_pages=0), INVALID),
+    (dict(heads=0), INVALID), (dict(heads=7), INVALID), (dict(heads=-8), INVALID),
+    (dict(softmax_scale=float("nan")), INVALID), (dict(softmax_scale=float("inf")), INVALID),
+    (dict(max_pages=1 << 27), UNSUPPORTED), (dict(heads=2 * 257), UNSUPPORTED), (dict(requests=65537), UNSUPPORTED),
+    (dict(q_stride=8 * 64 - 8), INVALID), (dict(q_stride=8 * 64 + 4), UNSUPPORTED),
+    (dict(q_stride=(1 << 31) + 8), UNSUPPORTED),
+]
+
+
+@fake_pointers
+@pytest.mark.parametrize("kw,status", BAD_ATTN)
+def test_attention_refuses_bad_descriptors(kw, status):
+    assert call_attn(attn(**kw)) == status
+    assert attn_bytes(attn(**kw)) == (status, 0)
+
+
+@fake_pointers
+@pytest.mark.parametrize("kw,status", BAD_CACHES)
+def test_attention_refuses_bad_caches(kw, status):
+    heads = 8 if kw.get("kv_heads", 2) != 5000 else 5000
+    assert call_attn(attn(cache(**kw), heads=heads)) == status
+
+
+@fake_pointers
+def test_attention_refusals():
+    d = attn()
+    assert call_attn(None) == INVALID
+    assert attn_bytes(None) == (INVALID, 0)
+    assert dlf.raw().dlf_paged_attention_workspace_bytes(ref(d), None) == INVALID
+    assert call_attn(attn(requests=0), q=None, out=None, workspace=None) == dlf.DLF_OK
+    for n in ("q", "k_cache", "v_cache", "block_table", "lens", "out"):
+        assert call_attn(d, **{n: None}) == INVALID, n
+    for n in ("q", "k_cache", "v_cache", "out"):
+        assert call_attn(d, **{n: addr(40, 8)}) == INVALID, n
+    for n in ("block_table", "lens", "lse"):
+        assert call_attn(d, **{n: addr(40, 2)}) == INVALID, n
+    rows = 4 * 8 * 64 * 2
+    assert call_attn(d, out=addr(0, rows - 16)) == ALIAS
+    assert call_attn(d, out=addr(1)) == ALIAS
+    assert call_attn(d, lse=addr(4, 12)) == ALIAS
+    assert call_attn(d, lse=addr(5, rows - 4)) == ALIAS
+    assert call_attn(attn(q_stride=1024), out=addr(0, (3 * 1024 + 512) * 2 - 16)) == ALIAS
+
+
+def test_attention_binding_checks_shapes():
+    torch = pytest.importorskip("torch")
+    d = attn()
+    q = torch.zeros(4, 8, 64, dtype=torch.bfloat16)
+    wide = torch.zeros(4, 1024, dtype=torch.bfloat16)[:, :512].unflatten(1, (8, 64))
+    i = torch.zeros(4, 4, dtype=torch.int32)
+    for bad in (q[:3], q[:, :4], q.transpose(0, 1), q[:, :, ::2], q.view(4, 512), wide):
+        with pytest.raises(ValueError):
+            dlf.dlf_paged_attention(d, bad, q, q, i, i[0], q, None, None, 0, stream=0)
