@@ -116,6 +116,18 @@ def paged_attn_desc(cache, requests, heads, max_pages, softmax_scale, window=0, 
                                heads * cache.head_dim if q_stride is None else q_stride, softmax_scale)
 
 
+class dlf_lora_desc(ctypes.Structure):
+    _fields_ = [("m", ctypes.c_int64), ("n", ctypes.c_int32), ("k", ctypes.c_int32), ("rank", ctypes.c_int32),
+                ("adapters", ctypes.c_int32), ("requests", ctypes.c_int32), ("x_stride", ctypes.c_int64),
+                ("base_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64), ("dtype", ctypes.c_int)]
+
+
+def lora_desc(m, n, k, rank, adapters, requests=0, x_stride=None, base_stride=None, out_stride=None, dtype="bf16"):
+    return dlf_lora_desc(m, n, k, rank, adapters, requests, k if x_stride is None else x_stride,
+                         n if base_stride is None else base_stride, n if out_stride is None else out_stride,
+                         DTYPES.get(dtype, dtype))
+
+
 class dlf_graph_node(ctypes.Structure):
     _fields_ = [("op", ctypes.c_int32), ("n_inputs", ctypes.c_int32), ("inputs", ctypes.c_int32 * 2),
                 ("dtype", ctypes.c_int32), ("flags", ctypes.c_uint32), ("rank", ctypes.c_int32),
@@ -155,6 +167,8 @@ _SIGS = {
     "dlf_paged_store": [ctypes.POINTER(dlf_kv_cache_desc), _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp],
     "dlf_paged_attention_workspace_bytes": [ctypes.POINTER(dlf_paged_attn_desc), ctypes.POINTER(ctypes.c_size_t)],
     "dlf_paged_attention": [ctypes.POINTER(dlf_paged_attn_desc)] + [_vp] * 8 + [ctypes.c_size_t, _vp],
+    "dlf_lora_workspace_bytes": [ctypes.POINTER(dlf_lora_desc), ctypes.POINTER(ctypes.c_size_t)],
+    "dlf_lora_add": [ctypes.POINTER(dlf_lora_desc)] + [_vp] * 9 + [ctypes.c_size_t, _vp],
     "dlf_clock_probe": [ctypes.c_int32, ctypes.c_int32, _vp, _vp],
     "dlf_fusion_plan": [ctypes.POINTER(dlf_graph_node), ctypes.c_int32, ctypes.c_double, ctypes.c_double,
                         ctypes.POINTER(dlf_fusion_group), ctypes.c_int32, ctypes.POINTER(ctypes.c_int32)],
@@ -409,6 +423,33 @@ def dlf_paged_attention(desc, q, k_cache, v_cache, block_table, lens, out, lse, 
     _check(_lib.dlf_paged_attention(ctypes.byref(desc), qp, _dev(k_cache), _dev(v_cache), _dev(block_table),
                                     _dev(lens), _dev(out), _dev(lse), _dev(workspace), int(workspace_bytes),
                                     _stream(stream)), "dlf_paged_attention")
+
+
+def dlf_lora_workspace_bytes(desc):
+    n = ctypes.c_size_t(0)
+    _check(_lib.dlf_lora_workspace_bytes(ctypes.byref(desc), ctypes.byref(n)), "dlf_lora_workspace_bytes")
+    return n.value
+
+
+def _matrix(t, rows, cols, stride, name):
+    """Device pointer of a [rows][cols] tensor whose rows are `stride` elements apart, or of a raw
+    address or None as it is."""
+    if t is None or isinstance(t, int):
+        return t
+    p, s = _rows(t, 2)
+    if t.shape[0] != rows or t.shape[1] != cols or (rows > 1 and s != stride):
+        raise ValueError(f"{name} must be [{rows}][{cols}] with rows {stride} elements apart")
+    return p
+
+
+def dlf_lora_add(desc, x, a, b, scale, ids, row_map, base, out, workspace, workspace_bytes, stream=None):
+    """out = base + scale (x A^T) B^T by each row's own adapter (see include/dlfusion.h); the rows of
+    x, base and out lie the descriptor's strides apart."""
+    _check(_lib.dlf_lora_add(ctypes.byref(desc), _matrix(x, desc.m, desc.k, desc.x_stride, "x"), _dev(a), _dev(b),
+                             _dev(scale), _dev(ids), _dev(row_map),
+                             _matrix(base, desc.m, desc.n, desc.base_stride, "base"),
+                             _matrix(out, desc.m, desc.n, desc.out_stride, "out"), _dev(workspace),
+                             int(workspace_bytes), _stream(stream)), "dlf_lora_add")
 
 
 def dlf_clock_probe(workgroups, iters, stamps, stream=None):

@@ -212,6 +212,24 @@ struct PagedAttnArgs {
 };
 hipError_t launch_paged_attention(const PagedAttnArgs& args, int head_dim, bool fp8, hipStream_t stream);
 
+// Low-rank adapters beside a projection (dlf_lora_add).
+struct LoraArgs {
+    const uint16_t* x;          // [m][k], rows x_stride apart
+    const uint16_t* a;          // [adapters][rank][k]
+    const uint16_t* b;          // [adapters][n][rank]
+    const float* scale;         // [adapters] or nullptr (= 1)
+    const int32_t* ids;         // [m], or [requests] with a row map
+    const int32_t* row_map;     // [m] or nullptr
+    const uint16_t* base;       // [m][n], rows base_stride apart, or nullptr
+    uint16_t* out;              // [m][n], rows out_stride apart
+    float* h;                   // workspace: [parts][m][rank] partial sums of x A^T
+    int64_t x_stride, base_stride, out_stride;
+    int m, n, k, rank, adapters, requests;
+    int parts;                  // k slices of the first product (lora_parts)
+};
+int lora_parts(int m, int k, int adapters);
+hipError_t launch_lora(const LoraArgs& args, hipStream_t stream);
+
 // Shader-clock probe: workgroups x 4 waves of back-to-back bf16 MFMAs; stamps[4 b + 0..3] =
 // s_memtime before / after, s_memrealtime before / after, for workgroup b.
 hipError_t launch_clock_probe(int workgroups, int iters, uint64_t* stamps, hipStream_t stream);

@@ -512,6 +512,52 @@ dlf_status dlf_paged_attention(const dlf_paged_attn_desc *d, const void *q, cons
                                void *stream);
 
 /* ---------------------------------------------------------------------- */
+/* Low-rank adapters of many requests beside a shared projection            */
+/* ---------------------------------------------------------------------- */
+
+/* Adapter i of a pool of `adapters` adds scale[i] x A_i^T B_i^T to a
+ * projection, with A_i [rank][k] and B_i [n][rank] ([out][in], as the weights
+ * of linear layers). */
+typedef struct {
+    int64_t m;                  /* rows (tokens) */
+    int32_t n, k;               /* the projection's outputs and inputs, multiples of 8, at most 2^23 */
+    int32_t rank;               /* a multiple of 8, at most 128 */
+    int32_t adapters;
+    int32_t requests;           /* entries of ids where a row map is given */
+    int64_t x_stride, base_stride, out_stride;  /* elements between rows, multiples of 8 */
+    dlf_dtype dtype;            /* DLF_BF16 (else DLF_ERR_UNSUPPORTED) */
+} dlf_lora_desc;
+
+/* Bytes of device workspace dlf_lora_add needs for d; checks, statuses and
+ * bytes as in dlf_paged_attention_workspace_bytes. */
+dlf_status dlf_lora_workspace_bytes(const dlf_lora_desc *d, size_t *bytes);
+
+/* For every row i with adapter a = ids[row_map ? row_map[i] : i]:
+ *     out[i] = base[i] + scale[a] * (x[i] A_a^T) B_a^T
+ * and out[i] = base[i] where a is not in [0, adapters) or row_map[i] not in
+ * [0, requests).  Rows may come in any order of their adapters.  The sums are
+ * fp32, the inner vector x A^T enters the second product as a sum of two bf16
+ * values, and out is rounded once.  As the residual of dlf_gemm_fused (base
+ * NULL, or the block's own residual) the sum with the projection is rounded
+ * once more at most by the adapter's own share; base == out adds to a finished
+ * projection in place.
+ *   x         device bf16 [m][k], rows x_stride apart
+ *   a, b      device bf16 [adapters][rank][k] and [adapters][n][rank]
+ *   scale     device fp32 [adapters] or NULL (= 1)
+ *   ids       device int32 [m], or [requests] with a row map
+ *   row_map   device int32 [m] or NULL: the rows of dlf_page_plan
+ *   base      device bf16 [m][n], rows base_stride apart, or NULL (= 0)
+ *   out       device bf16 [m][n], rows out_stride apart: either base itself with
+ *             its stride, or (else DLF_ERR_ALIAS) no overlap with any input
+ *   workspace device, 16-byte aligned, as for dlf_paged_attention
+ * UNSUPPORTED: n, k, rank or a stride not a multiple of 8, rank above 128,
+ * another dtype, m above 2^24, n or k above 2^23. */
+dlf_status dlf_lora_add(const dlf_lora_desc *d, const void *x, const void *a, const void *b,
+                        const float *scale, const int32_t *ids, const int32_t *row_map,
+                        const void *base, void *out, void *workspace, size_t workspace_bytes,
+                        void *stream);
+
+/* ---------------------------------------------------------------------- */
 /* Host fusion pass: which chains of a graph become one fused launch        */
 /* ---------------------------------------------------------------------- */
 

@@ -196,3 +196,87 @@ def test_attention_binding_checks_shapes():
     for bad in (q[:3], q[:, :4], q.transpose(0, 1), q[:, :, ::2], q.view(4, 512), wide):
         with pytest.raises(ValueError):
             dlf.dlf_paged_attention(d, bad, q, q, i, i[0], q, None, None, 0, stream=0)
+
+
+# ---------------------------------------------------------------------------
+# Adapters
+# ---------------------------------------------------------------------------
+LORA_PTRS = ("x", "a", "b", "scale", "ids", "row_map", "base", "out", "workspace")
+
+
+def lora(**kw):
+    args = dict(m=5, n=64, k=96, rank=16, adapters=3, requests=2)
+    args.update(kw)
+    return dlf.lora_desc(**args)
+
+
+def call_lora(d, ws_bytes=1 << 30, **ptrs):
+    p = {n: addr(i) for i, n in enumerate(LORA_PTRS)}
+    p.update(ptrs)
+    return dlf.raw().dlf_lora_add(ref(d), *[p[n] for n in LORA_PTRS], ws_bytes, None)
+
+
+def lora_bytes(d):
+    n = ctypes.c_size_t(123)
+    st = dlf.raw().dlf_lora_workspace_bytes(ref(d), ctypes.byref(n))
+    return st, n.value
+
+
+BAD_LORA = [
+    (dict(dtype="f32"), UNSUPPORTED), (dict(dtype="fp8"), UNSUPPORTED), (dict(dtype=9), INVALID),
+    (dict(m=-1), INVALID), (dict(n=-8), INVALID), (dict(k=-8), INVALID), (dict(rank=-8), INVALID),
+    (dict(adapters=-1), INVALID), (dict(requests=-1), INVALID), (dict(rank=0), UNSUPPORTED), (dict(rank=12), UNSUPPORTED),
+    (dict(rank=136), UNSUPPORTED), (dict(n=60), UNSUPPORTED), (dict(k=100), UNSUPPORTED),
+    (dict(n=(1 << 23) + 8), UNSUPPORTED), (dict(k=(1 << 23) + 8), UNSUPPORTED), (dict(m=(1 << 24) + 1), UNSUPPORTED),
+    (dict(x_stride=88), INVALID), (dict(base_stride=56), INVALID), (dict(out_stride=56), INVALID),
+    (dict(x_stride=100), UNSUPPORTED), (dict(base_stride=68), UNSUPPORTED), (dict(out_stride=(1 << 31) + 8), UNSUPPORTED),
+]
+
+
+@fake_pointers
+@pytest.mark.parametrize("kw,status", BAD_LORA)
+def test_adapters_refuse_bad_descriptors(kw, status):
+    assert call_lora(lora(**kw)) == status
+    assert lora_bytes(lora(**kw)) == (status, 0)
+
+
+@fake_pointers
+def test_adapters_refusals():
+    d = lora()
+    st, need = lora_bytes(d)
+    assert st == dlf.DLF_OK and need >= 5 * 16 * 4
+    assert call_lora(None) == INVALID and lora_bytes(None) == (INVALID, 0)
+    assert dlf.raw().dlf_lora_workspace_bytes(ref(d), None) == INVALID
+    assert call_lora(lora(m=0), x=None, out=None, workspace=None) == dlf.DLF_OK
+    assert call_lora(lora(n=0), out=None, workspace=None) == dlf.DLF_OK
+    assert lora_bytes(lora(m=0)) == (dlf.DLF_OK, 0)
+    for n in ("x", "a", "b", "ids", "out", "workspace"):
+        assert call_lora(d, **{n: None}) == INVALID, n
+    for n in ("x", "a", "b", "base", "out", "workspace"):
+        assert call_lora(d, **{n: addr(40, 8)}) == INVALID, n
+    for n in ("scale", "ids", "row_map"):
+        assert call_lora(d, **{n: addr(40, 2)}) == INVALID, n
+    assert call_lora(d, ws_bytes=need - 1) == INVALID
+    assert "workspace" in dlf.dlf_last_error()
+    for n, size in (("x", 5 * 96 * 2), ("a", 3 * 16 * 96 * 2), ("b", 3 * 16 * 64 * 2), ("scale", 12), ("ids", 8),
+                    ("row_map", 20)):
+        last = addr(LORA_PTRS.index(n), (size - 1) // 16 * 16)
+        assert call_lora(d, out=last) == ALIAS, n
+        assert call_lora(d, workspace=last) == ALIAS, n
+    # base may be out itself, not part of it, nor with another stride
+    base = addr(LORA_PTRS.index("base"))
+    assert call_lora(d, out=base + 128) == ALIAS
+    assert call_lora(lora(out_stride=128), out=base) == ALIAS
+    assert call_lora(d, workspace=base) == ALIAS
+    assert call_lora(d, workspace=addr(LORA_PTRS.index("out"))) == ALIAS
+
+
+def test_adapters_binding_checks_shapes():
+    torch = pytest.importorskip("torch")
+    d = lora()
+    x, y = torch.zeros(5, 96, dtype=torch.bfloat16), torch.zeros(5, 64, dtype=torch.bfloat16)
+    w = torch.zeros(4096, dtype=torch.uint8)
+    wide = torch.zeros(5, 128, dtype=torch.bfloat16)[:, :96]
+    for bx, by in ((x[:4], y), (wide, y), (x.t(), y), (x, y[:, :32]), (x, y.view(5, 8, 8))):
+        with pytest.raises(ValueError):
+            dlf.dlf_lora_add(d, bx, x, x, None, x, None, None, by, w, 4096, stream=0)
