@@ -203,13 +203,20 @@ struct PagedAttnArgs {
     const int32_t* lens;        // [requests]
     uint16_t* out;              // [requests][heads][head_dim]
     float* lse;                 // [requests][heads] or nullptr
+    // workspace, unused where aim is 0
+    float* part_o;              // [items + aim][min(group, 16)][head_dim]: the pieces' sums
+    float* part_ml;             // the same rows' maximum and sum
+    int32_t* pieces;            // [requests][2]: a request's first piece among all requests', and its pieces
     int64_t q_stride;
     int requests, heads, kv_heads, page_size, pages, max_pages, window;
     int group;                  // heads / kv_heads
     int head_tiles;             // ceil(group / 16)
+    int aim;                    // pieces that the items are cut into if they are long, 0: none is cut
+    int least;                  // tiles that are not cut further
     float score_scale;          // softmax_scale * k_scale * log2(e)
     float v_scale;
 };
+void plan_paged_attention(PagedAttnArgs* args, int max_len);   // fills aim and least
 hipError_t launch_paged_attention(const PagedAttnArgs& args, int head_dim, bool fp8, hipStream_t stream);
 
 // Low-rank adapters beside a projection (dlf_lora_add).

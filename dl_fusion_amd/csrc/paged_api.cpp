@@ -161,13 +161,27 @@ dlf_status check_attn_desc(const dlf_paged_attn_desc* d, dlf::PagedAttnArgs* a) 
     a->window = d->window;
     a->group = group;
     a->head_tiles = (group + 15) / 16;
-    if (static_cast<int64_t>(d->requests) * c->kv_heads * a->head_tiles >= (int64_t(1) << 31))
-        return fail(DLF_ERR_UNSUPPORTED, "requests * kv_heads must stay below 2^31");
+    if (static_cast<int64_t>(d->requests) * c->kv_heads * a->head_tiles >= (int64_t(1) << 31) ||
+        static_cast<int64_t>(d->requests) * d->heads >= (int64_t(1) << 31))
+        return fail(DLF_ERR_UNSUPPORTED, "requests * heads must stay below 2^31");
     const bool fp8 = c->dtype == DLF_FP8_E4M3;
     a->score_scale = static_cast<float>(static_cast<double>(d->softmax_scale) * (fp8 ? c->k_scale : 1.0f) *
                                         1.4426950408889634074);
     a->v_scale = fp8 ? c->v_scale : 1.0f;
+    dlf::plan_paged_attention(a, d->max_len);
     return ok();
+}
+
+// rows of the pieces' sums, where items are cut
+size_t attn_part_rows(const dlf::PagedAttnArgs& a) {
+    if (a.aim == 0) return 0;
+    const size_t items = static_cast<size_t>(a.requests) * static_cast<size_t>(a.kv_heads * a.head_tiles);
+    return (items + static_cast<size_t>(a.aim)) * static_cast<size_t>(a.group < 16 ? a.group : 16);
+}
+
+size_t attn_ws_bytes(const dlf::PagedAttnArgs& a, int head_dim) {
+    if (a.aim == 0) return 0;
+    return attn_part_rows(a) * (static_cast<size_t>(head_dim) + 2) * 4 + static_cast<size_t>(a.requests) * 8;
 }
 
 }  // namespace
@@ -176,7 +190,10 @@ extern "C" dlf_status dlf_paged_attention_workspace_bytes(const dlf_paged_attn_d
     if (!bytes) return fail(DLF_ERR_INVALID_ARG, "bytes is NULL");
     *bytes = 0;
     dlf::PagedAttnArgs a;
-    return check_attn_desc(d, &a);
+    const dlf_status st = check_attn_desc(d, &a);
+    if (st != DLF_OK) return st;
+    *bytes = d->requests > 0 ? attn_ws_bytes(a, d->cache.head_dim) : 0;
+    return ok();
 }
 
 extern "C" dlf_status dlf_paged_attention(const dlf_paged_attn_desc* d, const void* q, const void* k_cache,
@@ -197,10 +214,18 @@ extern "C" dlf_status dlf_paged_attention(const dlf_paged_attn_desc* d, const vo
     const dlf::Span ks{k_cache, cache_bytes(&d->cache)}, vs{v_cache, cache_bytes(&d->cache)};
     const dlf::Span ts{block_table, r * static_cast<size_t>(d->max_pages) * 4}, ls{lens, r * 4};
     const dlf::Span os{out, rows * width * 2}, es{lse, rows * 4};
-    if (any_overlap({os, es}, {qs, ks, vs, ts, ls}))
-        return fail(DLF_ERR_ALIAS, "an output overlaps an input or the other output");
-    (void)workspace;
-    (void)workspace_bytes;
+    const size_t part_rows = attn_part_rows(a), need = attn_ws_bytes(a, d->cache.head_dim);
+    if (need > 0) {
+        if (!workspace || workspace_bytes < need)
+            return fail(DLF_ERR_INVALID_ARG, "workspace of %zu bytes needed (dlf_paged_attention_workspace_bytes), got %zu",
+                        need, workspace ? workspace_bytes : size_t(0));
+        if (!aligned(workspace, 16)) return fail(DLF_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+    }
+    if (any_overlap({os, es, {workspace, need}}, {qs, ks, vs, ts, ls}))
+        return fail(DLF_ERR_ALIAS, "an output or the workspace overlaps an operand");
+    a.part_o = static_cast<float*>(workspace);
+    a.part_ml = need > 0 ? a.part_o + part_rows * width : nullptr;
+    a.pieces = need > 0 ? reinterpret_cast<int32_t*>(a.part_ml + part_rows * 2) : nullptr;
     a.q = static_cast<const uint16_t*>(q);
     a.k = static_cast<const uint8_t*>(k_cache);
     a.v = static_cast<const uint8_t*>(v_cache);

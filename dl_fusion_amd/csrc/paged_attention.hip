@@ -8,7 +8,9 @@
 // What bounds it is the read of the cache: 4 flops a value at bf16 and one query head, 64 at 16 of
 // them, against the hundreds a byte that the matrix cores could do.  So the products need no tuning
 // beyond keeping out of the way, and the layout is chosen so that nothing stands between a load and
-// the MFMA that uses it, no LDS and no lane exchange:
+// the MFMA that uses it, no LDS and no lane exchange.  64 uneven requests of up to 8191 tokens read
+// 698 MB in 124 us, 5.6 TB/s; two of 32768 and 131072 tokens 671 MB in 113 us, 5.9 TB/s (8 kv heads of
+// 128 dims), where a loop of nothing but these loads reads 6.0 TB/s in random pages.
 //  - scores are computed transposed, S^T = K Q^T (16 tokens x 16 queries an MFMA): a lane's key
 //    operand is 16 contiguous bytes of one token's row;
 //  - the 16x16 result leaves each lane with one query's scores of 4 tokens, which is just the
@@ -25,10 +27,31 @@
 namespace dlf {
 namespace {
 
-constexpr int kAttnWaves = 4;
 constexpr float kLn2 = 0.693147180559945309f;
+constexpr int kJoinThreads = 256;
 
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+
+constexpr int kWaves = 4;
+
+// What is read of a request: tokens [lo, len), in tiles of 32 from t16 on, lo rounded down to a
+// multiple of 16 so that 16 tokens share a page.
+struct Reach {
+    int len, lo, t16;
+    uint32_t tiles;     // 0 where there is no token
+};
+
+__device__ __forceinline__ Reach reach_of(const PagedAttnArgs& p, int r) {
+    const int64_t cap = static_cast<int64_t>(p.max_pages) * p.page_size;   // < 2^31
+    int len = p.lens[r];
+    len = len < 0 ? 0 : len > cap ? static_cast<int>(cap) : len;
+    const int lo = p.window > 0 && len > p.window ? len - p.window : 0;
+    const int t16 = lo & ~15;
+    return {len, lo, t16, (static_cast<uint32_t>(len - t16) + 31) / 32};
+}
+
+// Tiles that a request counts for in the split of the work: at least one, which writes its zeros.
+__device__ __forceinline__ uint32_t share_of(const Reach& k) { return k.tiles > 0 ? k.tiles : 1; }
 
 // The cache bytes of 32 tokens of one head as a wave holds them.
 template <int D, bool FP8>
@@ -37,7 +60,10 @@ struct KvTile {
     static constexpr int kKeyLoads = kRow / 64;         // 16-byte loads a lane and 16 tokens
     static constexpr int kValWords = kRow / 64;         // 32-bit words of a lane's 1/16 of a row
     u32x4_t k[2][kKeyLoads];
-    uint32_t v[8][kValWords];
+    typedef uint32_t value_t __attribute__((ext_vector_type(kValWords < 4 ? kValWords : 4)));
+    static constexpr int kValLoads = (kValWords + 3) / 4;
+    value_t v[8][kValLoads];
+    __device__ __forceinline__ uint32_t word(int token, int c) const { return v[token][c / 4][c & 3]; }
 };
 
 // Two bf16 values a word from two e4m3 codes (exact).
@@ -46,32 +72,118 @@ __device__ __forceinline__ uint32_t fp8x2_to_bf16x2(uint32_t codes) {
     return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, 1.0f, HIGH));
 }
 
-template <int D, bool FP8>
-__global__ __launch_bounds__(64 * kAttnWaves, D == 256 ? 1 : 2) void paged_attention_kernel(const PagedAttnArgs p) {
+// Inclusive sum over the wave's lanes: shifts by 1, 2, 4 and 8 within rows of 16 lanes, then the
+// rows' sums handed on; lanes without a source add 0.
+__device__ __forceinline__ uint32_t wave_scan(uint32_t x) {
+    x += __builtin_amdgcn_update_dpp(0u, x, 0x111, 0xF, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0u, x, 0x112, 0xF, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0u, x, 0x114, 0xF, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0u, x, 0x118, 0xF, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0u, x, 0x142, 0xA, 0xF, false);
+    x += __builtin_amdgcn_update_dpp(0u, x, 0x143, 0xC, 0xF, false);
+    return x;
+}
+
+// What a workgroup takes: tiles [tile, end) of request r, for one kv head and tile of its query heads.
+struct Work {
+    int r, head;
+    uint32_t tile, end;
+    int block, pieces;      // its number among the pieces of all requests, and those of its request
+};
+
+// Lengths are only known here, so the pieces are cut here: with `all` tiles in all items, an item is
+// cut into pieces of at most max(all / aim, least) tiles, equal ones within a request.  There are at
+// most aim + items of them, whatever the lengths.  Each wave adds the lengths up by itself: one load
+// and two scans of 64 lanes for up to 64 requests.
+__device__ __forceinline__ bool find_work(const PagedAttnArgs& p, int heads, int lane, Work* w) {
+    const int per = (p.requests + 63) / 64;
+    uint32_t mine = 0;
+    for (int i = 0; i < per; ++i) {
+        const int r = lane * per + i;
+        if (r < p.requests) mine += share_of(reach_of(p, r));
+    }
+    const uint32_t all = __builtin_amdgcn_readlane(wave_scan(mine), 63);      // < 2^31
+    const uint64_t even = (static_cast<uint64_t>(all) * static_cast<uint32_t>(heads) + static_cast<uint32_t>(p.aim) - 1) /
+                          static_cast<uint32_t>(p.aim);
+    uint32_t most = even < all ? static_cast<uint32_t>(even) : all;
+    most = most > static_cast<uint32_t>(p.least) ? most : static_cast<uint32_t>(p.least);
+    uint32_t cuts = 0;
+    for (int i = 0; i < per; ++i) {
+        const int r = lane * per + i;
+        if (r < p.requests) cuts += (share_of(reach_of(p, r)) + most - 1) / most;
+    }
+    const uint32_t upto = wave_scan(cuts);
+    const uint32_t at = blockIdx.x / static_cast<uint32_t>(heads);
+    const int first = __popcll(__ballot(upto <= at));
+    if (first == 64) return false;      // past the last piece
+    uint32_t before = __builtin_amdgcn_readlane(upto, first) - __builtin_amdgcn_readlane(cuts, first);
+    int r = first * per;
+    uint32_t share = share_of(reach_of(p, r)), n = (share + most - 1) / most;
+    while (before + n <= at) {
+        before += n;
+        share = share_of(reach_of(p, ++r));
+        n = (share + most - 1) / most;
+    }
+    const uint32_t size = (share + n - 1) / n;      // size <= most, so that (n - 1) size < share
+    w->r = r;
+    w->head = static_cast<int>(blockIdx.x - at * static_cast<uint32_t>(heads));
+    w->tile = (at - before) * size;
+    w->end = w->tile + size < share ? w->tile + size : share;
+    w->block = static_cast<int>(before);
+    w->pieces = static_cast<int>(n);
+    return true;
+}
+
+// CUT: items are cut into pieces, and those of more than one left to the join; else a workgroup
+// takes an item.
+template <int D, bool FP8, bool CUT>
+__global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? 3 : 4) void paged_attention_kernel(const PagedAttnArgs p) {
     using Tile = KvTile<D, FP8>;
     constexpr int kRow = Tile::kRow;
     constexpr int kSteps = D / 32;          // MFMA steps over the head's dims
     constexpr int kFrag = D / 16;           // dims a lane's value chunk holds = output fragments
-    __shared__ float o_s[kAttnWaves][16][D];
-    __shared__ float m_s[kAttnWaves][16], l_s[kAttnWaves][16];
+    constexpr int kPad = D + 4;             // floats of an LDS row: 16 rows in different banks
+    extern __shared__ float o_s[];          // [kWaves][rows][kPad]
+    __shared__ float m_s[kWaves][16], l_s[kWaves][16];
 
-    const int lane = static_cast<int>(threadIdx.x) & 63, wave = static_cast<int>(threadIdx.x) >> 6;
+    const int lane = static_cast<int>(threadIdx.x) & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
     const int qi = lane & 15, g = lane >> 4;
-    int item = static_cast<int>(blockIdx.x);
-    const int ht = item % p.head_tiles;
-    item /= p.head_tiles;
-    const int kvh = item % p.kv_heads, r = item / p.kv_heads;
+    const int heads = p.kv_heads * p.head_tiles, rows = p.group < 16 ? p.group : 16;
+    const uint32_t per_page = static_cast<uint32_t>(p.page_size) / 16;
+    const uint32_t key_lane = static_cast<uint32_t>(qi * kRow + 16 * g);
+    const uint32_t value_lane = static_cast<uint32_t>(4 * g * kRow + qi * (kRow / 16));
+
+    Work work;
+    if constexpr (CUT) {
+        if (!find_work(p, heads, lane, &work)) return;
+    } else {
+        work.r = static_cast<int>(blockIdx.x) / heads;
+        work.head = static_cast<int>(blockIdx.x) - work.r * heads;
+    }
+    const int r = work.r, kvh = work.head / p.head_tiles, ht = work.head - kvh * p.head_tiles;
     const int head0 = kvh * p.group + 16 * ht;                          // first query head of the tile
     const int nq = p.group - 16 * ht < 16 ? p.group - 16 * ht : 16;     // query heads in it
+    const Reach reach = reach_of(p, r);
+    const int len = reach.len, lo = reach.lo, t16 = reach.t16;
+    // this wave's tiles: first, first + kWaves, ..
+    const uint32_t first = (CUT ? work.tile : 0u) + static_cast<uint32_t>(wave);
+    const uint32_t end = CUT && work.end < reach.tiles ? work.end : reach.tiles;
+    const uint32_t tiles = first < end ? (end - first + kWaves - 1) / kWaves : 0;
 
-    // the tokens attended to: [lo, len); tiles start at a multiple of 16 so that 16 tokens share a page
-    const int64_t cap = static_cast<int64_t>(p.max_pages) * p.page_size;   // < 2^31
-    int len = p.lens[r];
-    len = len < 0 ? 0 : len > cap ? static_cast<int>(cap) : len;
-    const int lo = p.window > 0 && len > p.window ? len - p.window : 0;
-    const int t16 = lo & ~15;
-    const int tiles = (len - t16 + 31) / 32;
-    const int a = tiles * wave / kAttnWaves, b = tiles * (wave + 1) / kAttnWaves;
+    // byte offsets of the cache runs of the next 64 half tiles (16 tokens), one a lane; -1: no page
+    int64_t run = -1;
+    auto find_runs = [&](uint32_t i) {
+        const uint32_t at = 32 * (first + kWaves * (i + static_cast<uint32_t>(lane) / 2)) + 16u * (lane & 1);
+        const uint32_t h16 = (static_cast<uint32_t>(t16) + at) / 16, col = h16 / per_page;
+        run = -1;
+        if (at < static_cast<uint32_t>(len - t16)) {
+            const int32_t page = p.table[static_cast<int64_t>(r) * p.max_pages + col];
+            if (page >= 0 && page < p.pages)
+                run = ((static_cast<int64_t>(page) * p.kv_heads + kvh) * p.page_size + 16 * (h16 - col * per_page)) * kRow;
+        }
+    };
+    if (tiles > 0) find_runs(0);
 
     // query fragments: query qi, the dims that the key loads bring this lane
     bf16x8_t qf[kSteps];
@@ -90,55 +202,45 @@ __global__ __launch_bounds__(64 * kAttnWaves, D == 256 ? 1 : 2) void paged_atten
     for (int i = 0; i < kFrag; ++i) o[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
     float m = -INFINITY, l = 0.0f;      // l: this lane's share of the sum
 
-    // byte offsets of the cache runs of the next 64 half tiles (16 tokens), one a lane; -1: no page
-    const uint32_t per_page = static_cast<uint32_t>(p.page_size) / 16;
-    int64_t run = -1;
-    auto find_runs = [&](int tile) {
-        const int tok = t16 + 32 * tile + 16 * lane;
-        run = -1;
-        if (tok < len) {
-            const uint32_t h16 = static_cast<uint32_t>(tok) / 16, col = h16 / per_page;
-            const int32_t page = p.table[static_cast<int64_t>(r) * p.max_pages + col];
-            if (page >= 0 && page < p.pages)
-                run = ((static_cast<int64_t>(page) * p.kv_heads + kvh) * p.page_size + 16 * (h16 - col * per_page)) * kRow;
-        }
+    // where the two halves of tile i lie; a half without a page is read from the pool's start and masked
+    struct Where {
+        int64_t off[2];
+        bool there[2];
     };
-    // tile `tile` (wave-uniform) into registers; runs without a page are read from page 0 and masked
-    auto fetch = [&](int tile, Tile& t, bool (&there)[2]) {
-        if (((tile - a) & 31) == 0) find_runs(tile);
-        const int at = 2 * ((tile - a) & 31);
+    auto locate = [&](uint32_t i) {
+        Where w;
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
-            const int lo32 = __builtin_amdgcn_readlane(static_cast<int>(run), at + hh);
-            const int hi32 = __builtin_amdgcn_readlane(static_cast<int>(run >> 32), at + hh);
-            there[hh] = hi32 >= 0;
-            const int64_t off = there[hh] ? (static_cast<int64_t>(hi32) << 32) | static_cast<uint32_t>(lo32) : 0;
-            const uint8_t* const kp = p.k + off + qi * kRow + 16 * g;
+            const int lo32 = __builtin_amdgcn_readlane(static_cast<int>(run), static_cast<int>(2 * (i & 31)) + hh);
+            const int hi32 = __builtin_amdgcn_readlane(static_cast<int>(run >> 32), static_cast<int>(2 * (i & 31)) + hh);
+            w.there[hh] = hi32 >= 0;
+            w.off[hh] = w.there[hh] ? (static_cast<int64_t>(hi32) << 32) | static_cast<uint32_t>(lo32) : 0;
+        }
+        return w;
+    };
+    auto fetch_keys = [&](const Where& w, Tile& t) {
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+            const uint8_t* const kp = p.k + w.off[hh] + key_lane;
 #pragma unroll
             for (int s = 0; s < Tile::kKeyLoads; ++s) t.k[hh][s] = *reinterpret_cast<const u32x4_t*>(kp + 64 * s);
-            const uint8_t* const vp = p.v + off + 4 * g * kRow + qi * (kRow / 16);
+        }
+    };
+    auto fetch_values = [&](const Where& w, Tile& t) {
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+            const uint8_t* const vp = p.v + w.off[hh] + value_lane;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                uint32_t* const w = t.v[4 * hh + j];
-                if constexpr (Tile::kValWords == 1) {
-                    w[0] = *reinterpret_cast<const uint32_t*>(vp + j * kRow);
-                } else if constexpr (Tile::kValWords == 2) {
-                    const u32x2_t x = *reinterpret_cast<const u32x2_t*>(vp + j * kRow);
-                    w[0] = x[0];
-                    w[1] = x[1];
-                } else {
+                // a load's lanes cover whole lines: non-temporal ones read 6.8 TB/s against 6.0; the keys' loads,
+                // half a line each, lose by it
 #pragma unroll
-                    for (int c = 0; c < Tile::kValWords / 4; ++c) {
-                        const u32x4_t x = *reinterpret_cast<const u32x4_t*>(vp + j * kRow + 16 * c);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) w[4 * c + e] = x[e];
-                    }
-                }
+                for (int c = 0; c < Tile::kValLoads; ++c)
+                    t.v[4 * hh + j][c] = __builtin_nontemporal_load(reinterpret_cast<const typename Tile::value_t*>(vp + j * kRow + 16 * c));
             }
         }
     };
-    auto attend = [&](int tile, Tile& t, const bool (&there)[2]) {
-        f32x4_t sc[2];
+    auto scores = [&](const Tile& t, f32x4_t (&sc)[2]) {
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
             sc[hh] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
@@ -156,22 +258,23 @@ __global__ __launch_bounds__(64 * kAttnWaves, D == 256 ? 1 : 2) void paged_atten
                 sc[hh] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, kw), qf[s], sc[hh], 0, 0, 0);
             }
         }
-        // lane: query qi, tokens first + 16 hh + e
-        const int first = t16 + 32 * tile + 4 * g;
+    };
+    auto add_values = [&](const Where& w, uint32_t at, Tile& t, const f32x4_t (&sc)[2]) {
+        // lane: query qi, tokens tok0 + 16 hh + 4 g + e
+        const int tok0 = t16 + static_cast<int>(at);
         float z[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) z[i] = sc[i / 4][i & 3] * p.score_scale;
-        const int tok0 = t16 + 32 * tile;
-        if (tok0 < lo || tok0 + 32 > len || !there[0] || !there[1]) {
+        if (tok0 < lo || tok0 > len - 32 || !w.there[0] || !w.there[1]) {
             // masked tokens: the score is replaced, whatever it was, and the value row is cleared, since
             // 0 x NaN or 0 x inf of a stale slot would reach the sum
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const int tok = first + 16 * (i / 4) + (i & 3);
-                const bool seen = tok >= lo && tok < len && there[i / 4];
+                const uint32_t tok = static_cast<uint32_t>(tok0 + 4 * g) + 16 * (i / 4) + (i & 3);
+                const bool seen = tok >= static_cast<uint32_t>(lo) && tok < static_cast<uint32_t>(len) && w.there[i / 4];
                 z[i] = seen ? z[i] : -INFINITY;
 #pragma unroll
-                for (int w = 0; w < Tile::kValWords; ++w) t.v[i][w] = seen ? t.v[i][w] : 0u;
+                for (int c = 0; c < Tile::kValLoads; ++c) t.v[i][c] = seen ? t.v[i][c] : typename Tile::value_t(0u);
             }
         }
         float top = fmaxf(fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])), fmaxf(fmaxf(z[4], z[5]), fmaxf(z[6], z[7])));
@@ -181,7 +284,7 @@ __global__ __launch_bounds__(64 * kAttnWaves, D == 256 ? 1 : 2) void paged_atten
         const float base = mn == -INFINITY ? 0.0f : mn;     // nothing seen yet: every exp2 below is 0
         const float alpha = __builtin_amdgcn_exp2f(m - base);
         m = mn;
-        // p = hi + lo in bf16: the 2^-9 of one rounding would reach the output as much as its own rounding
+        // p = hi + lo in bf16: the 2^-8 of one rounding would reach the output as much as its own rounding
         float pr[8], lo_p[8], sum = 0.0f;
         uint32_t ph[4], pl[4];
 #pragma unroll
@@ -206,40 +309,62 @@ __global__ __launch_bounds__(64 * kAttnWaves, D == 256 ? 1 : 2) void paged_atten
             o[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf, o[i], 0, 0, 0);
             o[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pg, o[i], 0, 0, 0);
         };
-        // dims 2 w and 2 w + 1 of the lane's chunk, from one word of bf16 pairs of each token
-        auto pair = [&](int w, const uint32_t (&x)[8]) {
-            u32x4_t even, odd;
+        // dims of the lane's chunk, from one word of each of the 8 tokens: bytes of pairs of tokens are
+        // brought together, an e4m3 pair of two dims at a time before the conversion
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                even[i] = __builtin_amdgcn_perm(x[2 * i + 1], x[2 * i], 0x05040100u);
-                odd[i] = __builtin_amdgcn_perm(x[2 * i + 1], x[2 * i], 0x07060302u);
-            }
-            add(2 * w, even);
-            add(2 * w + 1, odd);
-        };
-#pragma unroll
-        for (int w = 0; w < Tile::kValWords; ++w) {
-            uint32_t x[8];
+        for (int c = 0; c < Tile::kValWords; ++c) {
             if constexpr (FP8) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = fp8x2_to_bf16x2<false>(t.v[i][w]);
-                pair(2 * w, x);
+                for (int half = 0; half < 2; ++half) {
+                    u32x4_t even, odd;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = fp8x2_to_bf16x2<true>(t.v[i][w]);
-                pair(2 * w + 1, x);
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t y = __builtin_amdgcn_perm(t.word(2 * i + 1, c), t.word(2 * i, c), half ? 0x07030602u : 0x05010400u);
+                        even[i] = fp8x2_to_bf16x2<false>(y);
+                        odd[i] = fp8x2_to_bf16x2<true>(y);
+                    }
+                    add(4 * c + 2 * half, even);
+                    add(4 * c + 2 * half + 1, odd);
+                }
             } else {
+                u32x4_t even, odd;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = t.v[i][w];
-                pair(w, x);
+                for (int i = 0; i < 4; ++i) {
+                    even[i] = __builtin_amdgcn_perm(t.word(2 * i + 1, c), t.word(2 * i, c), 0x05040100u);
+                    odd[i] = __builtin_amdgcn_perm(t.word(2 * i + 1, c), t.word(2 * i, c), 0x07060302u);
+                }
+                add(2 * c, even);
+                add(2 * c + 1, odd);
             }
         }
     };
 
-    Tile t;
-    bool there[2];
-    for (int tile = a; tile < b; ++tile) {
-        fetch(tile, t, there);
-        attend(tile, t, there);
+    // A tile's registers are refilled as they fall free, the keys after its scores, the values after
+    // the sums: something is always in flight.  The last tile is peeled so that every fetch in the
+    // loop is unconditional, which keeps the waits exact.
+    if (tiles > 0) {
+        Tile t;
+        f32x4_t sc[2];
+        Where w = locate(0);
+        fetch_keys(w, t);
+        __builtin_amdgcn_sched_barrier(0);
+        fetch_values(w, t);
+        __builtin_amdgcn_sched_barrier(0);
+        uint32_t at = 32 * first;
+        for (uint32_t i = 1; i < tiles; ++i) {
+            if ((i & 31) == 0) find_runs(i);
+            const Where next = locate(i);
+            scores(t, sc);
+            __builtin_amdgcn_sched_barrier(0);      // a fetch moved up would need registers of its own
+            fetch_keys(next, t);
+            add_values(w, at, t, sc);
+            __builtin_amdgcn_sched_barrier(0);
+            fetch_values(next, t);
+            w = next;
+            at += 32 * kWaves;
+        }
+        scores(t, sc);
+        add_values(w, at, t, sc);
     }
 
     // ---- the waves' results joined through LDS ----
@@ -254,22 +379,30 @@ __global__ __launch_bounds__(64 * kAttnWaves, D == 256 ? 1 : 2) void paged_atten
 #pragma unroll
         for (int e = 0; e < 4; ++e)
 #pragma unroll
-            for (int i = 0; i < kFrag; ++i) o_s[wave][qi][kFrag * (4 * g + e) + i] = o[i][e];
+            for (int i = 0; i < kFrag; ++i) o_s[(wave * rows + qi) * kPad + kFrag * (4 * g + e) + i] = o[i][e];
     }
     __syncthreads();
-    for (int i = static_cast<int>(threadIdx.x); i < nq * D / 2; i += 64 * kAttnWaves) {
+    if (CUT && threadIdx.x == 0 && work.head == 0 && work.tile == 0)
+        *reinterpret_cast<int2*>(p.pieces + 2 * r) = make_int2(work.block, work.pieces);      // for the join
+    for (int i = static_cast<int>(threadIdx.x); i < nq * D / 2; i += 64 * kWaves) {
         const int row = i / (D / 2), dim = 2 * (i % (D / 2));
         float top = m_s[0][row];
 #pragma unroll
-        for (int w = 1; w < kAttnWaves; ++w) top = fmaxf(top, m_s[w][row]);
+        for (int w = 1; w < kWaves; ++w) top = fmaxf(top, m_s[w][row]);
         const float base = top == -INFINITY ? 0.0f : top;
         float x = 0.0f, y = 0.0f, sum = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kAttnWaves; ++w) {
+        for (int w = 0; w < kWaves; ++w) {
             const float f = __builtin_amdgcn_exp2f(m_s[w][row] - base);
-            x += f * o_s[w][row][dim];
-            y += f * o_s[w][row][dim + 1];
+            x += f * o_s[(w * rows + row) * kPad + dim];
+            y += f * o_s[(w * rows + row) * kPad + dim + 1];
             sum += f * l_s[w][row];
+        }
+        if (CUT && work.pieces > 1) {
+            const int64_t at = static_cast<int64_t>(blockIdx.x) * rows + row;
+            *reinterpret_cast<f32x2_t*>(p.part_o + at * D + dim) = f32x2_t{x, y};
+            if (dim == 0) *reinterpret_cast<f32x2_t*>(p.part_ml + 2 * at) = f32x2_t{top, sum};
+            continue;
         }
         // no token left: zeros.  A sum of NaN is not 0 and goes through.
         const float inv = sum == 0.0f ? 0.0f : p.v_scale / sum;
@@ -279,14 +412,100 @@ __global__ __launch_bounds__(64 * kAttnWaves, D == 256 ? 1 : 2) void paged_atten
     }
 }
 
+// The pieces of an item joined: a workgroup per request and query head, a thread 4 dims of every
+// kJoinThreads * 4 / D-th piece.
+template <int D>
+__global__ __launch_bounds__(kJoinThreads) void paged_attention_join_kernel(const PagedAttnArgs p) {
+    constexpr int kAcross = D / 4, kDown = kJoinThreads / kAcross;
+    __shared__ f32x4_t o_s[kDown][kAcross];
+    __shared__ float l_s[kDown], m_s[kJoinThreads / 64];
+    const int r = static_cast<int>(blockIdx.x) / p.heads, h = static_cast<int>(blockIdx.x) - r * p.heads;
+    const int2 held = *reinterpret_cast<const int2*>(p.pieces + 2 * r);
+    const int mine = held.y;
+    if (mine == 1) return;      // written by the one workgroup
+    const int kvh = h / p.group, q = h - kvh * p.group;
+    const int rows = p.group < 16 ? p.group : 16, heads = p.kv_heads * p.head_tiles;
+    auto place = [&](int s) {
+        return (static_cast<int64_t>(held.x + s) * heads + kvh * p.head_tiles + q / 16) * rows + q % 16;
+    };
+    const int tid = static_cast<int>(threadIdx.x);
+    float top = -INFINITY;
+    for (int s = tid; s < mine; s += kJoinThreads) top = fmaxf(top, p.part_ml[2 * place(s)]);
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
+    if ((tid & 63) == 0) m_s[tid / 64] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kJoinThreads / 64; ++w) top = fmaxf(top, m_s[w]);
+    const float base = top == -INFINITY ? 0.0f : top;
+    const int c = tid % kAcross, down = tid / kAcross;
+    f32x4_t o{0.0f, 0.0f, 0.0f, 0.0f};
+    float sum = 0.0f;
+#pragma unroll 4
+    for (int s = down; s < mine; s += kDown) {
+        const int64_t at = place(s);
+        const f32x2_t ml = *reinterpret_cast<const f32x2_t*>(p.part_ml + 2 * at);
+        const f32x4_t x = *reinterpret_cast<const f32x4_t*>(p.part_o + at * D + 4 * c);
+        const float f = __builtin_amdgcn_exp2f(ml[0] - base);
+        sum += f * ml[1];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] += f * x[e];
+    }
+    o_s[down][c] = o;
+    if (c == 0) l_s[down] = sum;
+    __syncthreads();
+    if (tid >= kAcross) return;
+    o = o_s[0][tid];
+    sum = l_s[0];
+#pragma unroll
+    for (int w = 1; w < kDown; ++w) {
+        const f32x4_t x = o_s[w][tid];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] += x[e];
+        sum += l_s[w];
+    }
+    const float inv = sum == 0.0f ? 0.0f : p.v_scale / sum;
+    const int64_t row_at = static_cast<int64_t>(r) * p.heads + h;
+    *reinterpret_cast<uint2*>(p.out + row_at * D + 4 * tid) =
+        make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
+    if (p.lse && tid == 0) p.lse[row_at] = sum == 0.0f ? -INFINITY : kLn2 * (base + __builtin_amdgcn_logf(sum));
+}
+
 template <int D, bool FP8>
 hipError_t launch(const PagedAttnArgs& a, hipStream_t s) {
-    const int64_t items = static_cast<int64_t>(a.requests) * a.kv_heads * a.head_tiles;
-    paged_attention_kernel<D, FP8><<<static_cast<unsigned>(items), 64 * kAttnWaves, 0, s>>>(a);
+    const int rows = a.group < 16 ? a.group : 16;
+    const unsigned lds = static_cast<unsigned>(kWaves * rows * (D + 4) * 4);
+    const unsigned items = static_cast<unsigned>(a.requests) * static_cast<unsigned>(a.kv_heads * a.head_tiles);
+    if (a.aim == 0) {
+        paged_attention_kernel<D, FP8, false><<<items, 64 * kWaves, lds, s>>>(a);
+        return hipGetLastError();
+    }
+    paged_attention_kernel<D, FP8, true><<<items + static_cast<unsigned>(a.aim), 64 * kWaves, lds, s>>>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    paged_attention_join_kernel<D><<<static_cast<unsigned>(a.requests) * static_cast<unsigned>(a.heads), kJoinThreads, 0, s>>>(a);
     return hipGetLastError();
 }
 
 }  // namespace
+
+// Items are cut where the longest may pass 512 tokens.  Measured at 8 kv heads of 128 dims (us, whole
+// | cut): one request of 256 tokens 5.8 | 9.2, 512 8.0 | 9.3, 1024 13.0 | 9.6, 2048 24 | 10.7; 64 uneven
+// requests of up to 512 tokens 15 | 19, 1024 27 | 27, 2048 46 | 38, 8191 159 | 122.  Beyond 4096 items
+// the items alone are 4 rounds of what the chip holds.
+// 1024 pieces, 4 a CU: 512 lost up to 9% (the last ones leave CUs idle), 2048 up to 7% where there are
+// few kv heads and heads of 256 dims (beginnings and ends of pieces), and gained at most 4% elsewhere.
+// A piece has at least a tile a wave.
+void plan_paged_attention(PagedAttnArgs* a, int max_len) {
+    constexpr int kWhole = 512, kMaxItems = 4096, kPieces = 1024;
+    int64_t reach = static_cast<int64_t>(a->max_pages) * a->page_size;
+    const int64_t tiles = a->requests * (reach / 32 + 1);
+    if (max_len > 0 && max_len < reach) reach = max_len;
+    if (a->window > 0 && a->window < reach) reach = a->window;
+    const int64_t items = static_cast<int64_t>(a->requests) * a->kv_heads * a->head_tiles;
+    a->least = kWaves;
+    a->aim = reach <= kWhole || items > kMaxItems || tiles >= (int64_t(1) << 31) ? 0 : kPieces;
+}
 
 hipError_t launch_paged_attention(const PagedAttnArgs& a, int head_dim, bool fp8, hipStream_t s) {
     switch (head_dim) {

@@ -471,8 +471,9 @@ typedef struct {
                                  * kv head h / (heads / kv_heads) */
     int32_t max_pages;          /* columns of block_table */
     int32_t window;             /* 0, or the last tokens that a request attends to */
-    int32_t max_len;            /* 0, or an upper bound of lens known to the host: chooses the
-                                 * launch, never the result */
+    int32_t max_len;            /* 0, or an upper bound of lens known to the host: up to 512 the
+                                 * requests are not cut into pieces, which saves a launch and the
+                                 * workspace.  A wrong one costs time only */
     int64_t q_stride;           /* elements between two requests' queries, a multiple of 8 */
     float softmax_scale;
 } dlf_paged_attn_desc;
@@ -492,8 +493,9 @@ dlf_status dlf_paged_attention_workspace_bytes(const dlf_paged_attn_desc *d, siz
  * left has out = 0 and lse = -inf.  Cache slots past a request's length are
  * never used, whatever they hold.  Scores, statistics and sums are fp32; the
  * probabilities enter the second product as a sum of two bf16 values (2^-17
- * relative), and out is rounded once.  Keys or values in range that are not
- * finite give outputs that are not finite.
+ * relative), and out is rounded once.  The order of the sums depends on the
+ * lengths and the descriptor alone: the same inputs give the same bits.  A NaN
+ * in a key or value in range reaches the outputs that use it.
  *   q            device bf16 [requests][heads][head_dim], requests q_stride apart
  *   k_cache, v_cache  device, laid out as in dlf_kv_cache_desc
  *   block_table  device [requests][max_pages] int32

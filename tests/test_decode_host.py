@@ -187,6 +187,24 @@ def test_attention_refusals():
     assert call_attn(attn(q_stride=1024), out=addr(0, (3 * 1024 + 512) * 2 - 16)) == ALIAS
 
 
+@fake_pointers
+def test_attention_workspace():
+    """Needed where a request may be long enough to be cut, whatever says how long it may be."""
+    for kw in (dict(max_pages=4, page=16), dict(max_pages=1 << 16, max_len=512), dict(max_pages=1 << 16, window=512),
+               dict(max_pages=1 << 16, requests=5000), dict(max_pages=1 << 16, requests=0)):
+        page = kw.pop("page", 16)
+        assert attn_bytes(attn(cache(page_size=page), **kw)) == (dlf.DLF_OK, 0), kw
+    d = attn(max_pages=1 << 16)
+    st, need = attn_bytes(d)
+    assert st == dlf.DLF_OK and need > 0
+    assert call_attn(d, workspace=None) == INVALID and "workspace" in dlf.dlf_last_error()
+    assert call_attn(d, ws_bytes=need - 1) == INVALID
+    assert call_attn(d, workspace=addr(40, 8)) == INVALID
+    for i, n in enumerate(ATTN_PTRS):
+        if n != "workspace":
+            assert call_attn(d, workspace=addr(i)) == ALIAS, n
+
+
 def test_attention_binding_checks_shapes():
     torch = pytest.importorskip("torch")
     d = attn()

@@ -255,3 +255,46 @@ def test_graph_replays_follow_the_lengths():
         assert torch.equal(got, eager)
         ref, tol, _, _ = definition(s, 0.1)
         assert ((got.double() - ref).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("requests,kv_heads", [(63, 2), (65, 2), (300, 3), (1100, 2), (4200, 1)])
+def test_many_requests_of_which_few_are_long(requests, kv_heads):
+    """Pieces are cut over any number of requests (a table of 101 pages lets any be long); past 4096
+    items none is cut."""
+    print(f"attention requests={requests} kv_heads={kv_heads}, two long", flush=True)
+    lens = [(5 * i * i) % 23 for i in range(requests)]
+    lens[requests // 2], lens[-1] = 1600, 777
+    check(make(lens, 2 * kv_heads, kv_heads, 64, 16, cols=101), 0.125)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+@pytest.mark.parametrize("window", [513, 600, 5000])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_windows_over_pieces(dim, window, dtype):
+    print(f"attention window={window} dim={dim} {dtype}, pieces", flush=True)
+    check(make([6000, 512, 513, 0, 5001, 601, 1], 6, 2, dim, 48, dtype), dim ** -0.5, window=window)
+
+
+@pytest.mark.parametrize("heads,kv_heads", [(16, 1), (17, 1), (40, 2), (5, 5)])
+def test_head_layouts_over_pieces(heads, kv_heads):
+    print(f"attention heads={heads}/{kv_heads}, pieces", flush=True)
+    check(make([3000, 0, 1, 700], heads, kv_heads, 128, 32), 0.1)
+
+
+def test_a_piece_without_a_page():
+    """A long request whose pages are missing over whole pieces of it, and one without any."""
+    s = make([20000, 3000, 40], 4, 2, 64, 16, cols=1300)
+    s["table"][0, 100:1100] = -1
+    s["table"][1, :] = -1
+    skip = {(0, c) for c in range(100, 1100)} | {(1, c) for c in range(1300)}
+    print("attention pieces without pages", flush=True)
+    check(s, 0.125, skip=skip)
+
+
+def test_repeats_give_the_same_bits():
+    s = make([9000, 3, 0, 2050, 1, 700], 8, 2, 128, 16)
+    dev = device(s)
+    a, la = attend(s, 0.1, dev=dev)
+    for _ in range(3):
+        b, lb = attend(s, 0.1, dev=dev)
+        assert torch.equal(a, b) and torch.equal(la, lb)
