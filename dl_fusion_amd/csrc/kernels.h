@@ -216,7 +216,7 @@ struct PagedAttnArgs {
     float score_scale;          // softmax_scale * k_scale * log2(e)
     float v_scale;
 };
-void plan_paged_attention(PagedAttnArgs* args, int max_len);   // fills aim and least
+void plan_paged_attention(PagedAttnArgs* args, int row_bytes, int max_len);   // fills aim and least
 hipError_t launch_paged_attention(const PagedAttnArgs& args, int head_dim, bool fp8, hipStream_t stream);
 
 // Low-rank adapters beside a projection (dlf_lora_add).

@@ -168,7 +168,7 @@ dlf_status check_attn_desc(const dlf_paged_attn_desc* d, dlf::PagedAttnArgs* a) 
     a->score_scale = static_cast<float>(static_cast<double>(d->softmax_scale) * (fp8 ? c->k_scale : 1.0f) *
                                         1.4426950408889634074);
     a->v_scale = fp8 ? c->v_scale : 1.0f;
-    dlf::plan_paged_attention(a, d->max_len);
+    dlf::plan_paged_attention(a, c->head_dim * (fp8 ? 1 : 2), d->max_len);
     return ok();
 }
 

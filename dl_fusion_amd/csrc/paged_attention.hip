@@ -7,10 +7,10 @@
 //
 // What bounds it is the read of the cache: 4 flops a value at bf16 and one query head, 64 at 16 of
 // them, against the hundreds a byte that the matrix cores could do.  So the products need no tuning
-// beyond keeping out of the way, and the layout is chosen so that nothing stands between a load and
-// the MFMA that uses it, no LDS and no lane exchange.  64 uneven requests of up to 8191 tokens read
-// 698 MB in 124 us, 5.6 TB/s; two of 32768 and 131072 tokens 671 MB in 113 us, 5.9 TB/s (8 kv heads of
-// 128 dims), where a loop of nothing but these loads reads 6.0 TB/s in random pages.
+// beyond keeping out of the way, and the layout is chosen so that little stands between a load and
+// the MFMA that uses it: the keys pass through LDS, the values only through a byte permute.  64 uneven requests of up to 8191 tokens read
+// 698 MB in 118 us, 5.9 TB/s; two of 32768 and 131072 tokens 671 MB in 113 us, 5.9 TB/s (8 kv heads of
+// 128 dims); a loop of nothing but such loads reads 6.8 TB/s in random pages.
 //  - scores are computed transposed, S^T = K Q^T (16 tokens x 16 queries an MFMA): a lane's key
 //    operand is 16 contiguous bytes of one token's row;
 //  - the 16x16 result leaves each lane with one query's scores of 4 tokens, which is just the
@@ -53,17 +53,29 @@ __device__ __forceinline__ Reach reach_of(const PagedAttnArgs& p, int r) {
 // Tiles that a request counts for in the split of the work: at least one, which writes its zeros.
 __device__ __forceinline__ uint32_t share_of(const Reach& k) { return k.tiles > 0 ? k.tiles : 1; }
 
-// The cache bytes of 32 tokens of one head as a wave holds them.
+// The cache bytes of 32 tokens of one head, as a wave holds them: the keys in LDS, the values in
+// registers.
+//
+// A lane's key operand is 16 bytes of one token's row, and the 16 lanes next to each other have 16
+// tokens: loaded straight to registers that is 64 accesses of the cache to a load, and 58 GB/s a CU
+// was all it gave.  So keys go to LDS by loads of whole lines, no register between, and come back with
+// one 16-byte read a lane.  A row's 16-byte chunk c lies at place c ^ swizzle(row), so that the 16
+// lanes' reads fall on all banks: the lanes of the load take their chunks in that order.
 template <int D, bool FP8>
 struct KvTile {
     static constexpr int kRow = D * (FP8 ? 1 : 2);      // bytes of a token's row
-    static constexpr int kKeyLoads = kRow / 64;         // 16-byte loads a lane and 16 tokens
+    static constexpr int kBytes = 32 * kRow;            // the keys of a tile
+    static constexpr int kChunks = kRow / 16;
+    static constexpr int kKeyReads = kRow / 64;         // 16-byte reads a lane and 16 tokens
+    static constexpr int kKeyLoads = kRow / 64;         // 1 KB loads to LDS for 16 tokens
     static constexpr int kValWords = kRow / 64;         // 32-bit words of a lane's 1/16 of a row
-    u32x4_t k[2][kKeyLoads];
     typedef uint32_t value_t __attribute__((ext_vector_type(kValWords < 4 ? kValWords : 4)));
     static constexpr int kValLoads = (kValWords + 3) / 4;
     value_t v[8][kValLoads];
     __device__ __forceinline__ uint32_t word(int token, int c) const { return v[token][c / 4][c & 3]; }
+    static __device__ __forceinline__ int swizzle(int row) {
+        return kChunks >= 16 ? row & 15 : (row / (16 / kChunks)) & (kChunks - 1);
+    }
 };
 
 // Two bf16 values a word from two e4m3 codes (exact).
@@ -137,13 +149,15 @@ __device__ __forceinline__ bool find_work(const PagedAttnArgs& p, int heads, int
 // CUT: items are cut into pieces, and those of more than one left to the join; else a workgroup
 // takes an item.
 template <int D, bool FP8, bool CUT>
-__global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? 3 : 4) void paged_attention_kernel(const PagedAttnArgs p) {
+__global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : D == 128 ? 3 : 4) void paged_attention_kernel(const PagedAttnArgs p) {
     using Tile = KvTile<D, FP8>;
     constexpr int kRow = Tile::kRow;
     constexpr int kSteps = D / 32;          // MFMA steps over the head's dims
     constexpr int kFrag = D / 16;           // dims a lane's value chunk holds = output fragments
     constexpr int kPad = D + 4;             // floats of an LDS row: 16 rows in different banks
-    extern __shared__ float o_s[];          // [kWaves][rows][kPad]
+    // the waves' keys, and after them the waves' sums [kWaves][rows][kPad]
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    float* const o_s = reinterpret_cast<float*>(lds);
     __shared__ float m_s[kWaves][16], l_s[kWaves][16];
 
     const int lane = static_cast<int>(threadIdx.x) & 63;
@@ -151,7 +165,18 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? 3 : 4) void 
     const int qi = lane & 15, g = lane >> 4;
     const int heads = p.kv_heads * p.head_tiles, rows = p.group < 16 ? p.group : 16;
     const uint32_t per_page = static_cast<uint32_t>(p.page_size) / 16;
-    const uint32_t key_lane = static_cast<uint32_t>(qi * kRow + 16 * g);
+    // key loads: where lane's 16 bytes of the n-th KB of 16 tokens come from; key reads: where the chunks
+    // 4 s + g of token qi lie
+    uint32_t key_from[Tile::kKeyLoads], key_at[Tile::kKeyReads];
+#pragma unroll
+    for (int n = 0; n < Tile::kKeyLoads; ++n) {
+        const int row = (1024 * n + 16 * lane) / kRow, place = lane & (Tile::kChunks < 64 ? Tile::kChunks - 1 : 63);
+        key_from[n] = static_cast<uint32_t>(row * kRow + 16 * (place ^ Tile::swizzle(row)));
+    }
+#pragma unroll
+    for (int s = 0; s < Tile::kKeyReads; ++s)
+        key_at[s] = static_cast<uint32_t>(qi * kRow + 16 * ((4 * s + g) ^ Tile::swizzle(qi)));
+    uint8_t* const keys = lds + wave * Tile::kBytes;
     const uint32_t value_lane = static_cast<uint32_t>(4 * g * kRow + qi * (kRow / 16));
 
     Work work;
@@ -218,12 +243,13 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? 3 : 4) void 
         }
         return w;
     };
-    auto fetch_keys = [&](const Where& w, Tile& t) {
+    auto fetch_keys = [&](const Where& w) {
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
-            const uint8_t* const kp = p.k + w.off[hh] + key_lane;
+            const __amdgpu_buffer_rsrc_t rsrc = buffer_rsrc(p.k + w.off[hh], 16 * kRow);
 #pragma unroll
-            for (int s = 0; s < Tile::kKeyLoads; ++s) t.k[hh][s] = *reinterpret_cast<const u32x4_t*>(kp + 64 * s);
+            for (int n = 0; n < Tile::kKeyLoads; ++n)
+                load_lds16_stream(rsrc, key_from[n], keys + (16 * hh * kRow + 1024 * n));
         }
     };
     auto fetch_values = [&](const Where& w, Tile& t) {
@@ -232,32 +258,36 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? 3 : 4) void 
             const uint8_t* const vp = p.v + w.off[hh] + value_lane;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                // a load's lanes cover whole lines: non-temporal ones read 6.8 TB/s against 6.0; the keys' loads,
-                // half a line each, lose by it
+                // a load's lanes cover whole lines: non-temporal ones read 6.8 TB/s against 6.0
 #pragma unroll
                 for (int c = 0; c < Tile::kValLoads; ++c)
                     t.v[4 * hh + j][c] = __builtin_nontemporal_load(reinterpret_cast<const typename Tile::value_t*>(vp + j * kRow + 16 * c));
             }
         }
     };
-    auto scores = [&](const Tile& t, f32x4_t (&sc)[2]) {
+    auto scores = [&](f32x4_t (&sc)[2]) {
+        u32x4_t kw[Tile::kKeyReads][2];
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-            sc[hh] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int s = 0; s < Tile::kKeyReads; ++s)
 #pragma unroll
-            for (int s = 0; s < kSteps; ++s) {
-                u32x4_t kw;
+            for (int hh = 0; hh < 2; ++hh) kw[s][hh] = *reinterpret_cast<const u32x4_t*>(keys + 16 * hh * kRow + key_at[s]);
+        // all reads on their way before the first is waited for, where there are registers for it
+        if constexpr (Tile::kKeyReads <= 4) __builtin_amdgcn_sched_barrier(0);
+        sc[0] = sc[1] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) {
+                u32x4_t k;
                 if constexpr (FP8) {
-                    const u32x4_t x = t.k[hh][s / 2];
-                    const uint32_t c0 = x[2 * (s & 1)], c1 = x[2 * (s & 1) + 1];
-                    kw = u32x4_t{fp8x2_to_bf16x2<false>(c0), fp8x2_to_bf16x2<true>(c0), fp8x2_to_bf16x2<false>(c1),
-                                 fp8x2_to_bf16x2<true>(c1)};
+                    const uint32_t c0 = kw[s / 2][hh][2 * (s & 1)], c1 = kw[s / 2][hh][2 * (s & 1) + 1];
+                    k = u32x4_t{fp8x2_to_bf16x2<false>(c0), fp8x2_to_bf16x2<true>(c0), fp8x2_to_bf16x2<false>(c1),
+                                fp8x2_to_bf16x2<true>(c1)};
                 } else {
-                    kw = t.k[hh][s];
+                    k = kw[s][hh];
                 }
-                sc[hh] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, kw), qf[s], sc[hh], 0, 0, 0);
+                sc[hh] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, k), qf[s], sc[hh], 0, 0, 0);
             }
-        }
     };
     auto add_values = [&](const Where& w, uint32_t at, Tile& t, const f32x4_t (&sc)[2]) {
         // lane: query qi, tokens tok0 + 16 hh + 4 g + e
@@ -339,14 +369,16 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? 3 : 4) void 
         }
     };
 
-    // A tile's registers are refilled as they fall free, the keys after its scores, the values after
-    // the sums: something is always in flight.  The last tile is peeled so that every fetch in the
-    // loop is unconditional, which keeps the waits exact.
+    // A tile's LDS and registers are refilled as they fall free, the keys after its scores, the values
+    // after the sums: something is always in flight.  The last tile is peeled so that every fetch in the
+    // loop is unconditional, which keeps the waits exact: the keys have landed once at most the values'
+    // loads, which were issued after them, are outstanding.
+    constexpr int kValueLoads = 8 * Tile::kValLoads;
     if (tiles > 0) {
         Tile t;
         f32x4_t sc[2];
         Where w = locate(0);
-        fetch_keys(w, t);
+        fetch_keys(w);
         __builtin_amdgcn_sched_barrier(0);
         fetch_values(w, t);
         __builtin_amdgcn_sched_barrier(0);
@@ -354,22 +386,28 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : D == 128 ? 3 : 4) void 
         for (uint32_t i = 1; i < tiles; ++i) {
             if ((i & 31) == 0) find_runs(i);
             const Where next = locate(i);
-            scores(t, sc);
-            __builtin_amdgcn_sched_barrier(0);      // a fetch moved up would need registers of its own
-            fetch_keys(next, t);
+            __builtin_amdgcn_sched_barrier(0);
+            wait_vmcnt<kValueLoads>();
+            scores(sc);
+            __builtin_amdgcn_sched_barrier(0);      // the tile's reads are done
+            fetch_keys(next);
+            __builtin_amdgcn_sched_barrier(0);
             add_values(w, at, t, sc);
             __builtin_amdgcn_sched_barrier(0);
             fetch_values(next, t);
+            __builtin_amdgcn_sched_barrier(0);
             w = next;
             at += 32 * kWaves;
         }
-        scores(t, sc);
+        wait_vmcnt<kValueLoads>();
+        scores(sc);
         add_values(w, at, t, sc);
     }
 
     // ---- the waves' results joined through LDS ----
     l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
+    __syncthreads();        // no wave reads keys any more
     if (qi < nq) {
         if (g == 0) {
             m_s[wave][qi] = m;
@@ -474,7 +512,8 @@ __global__ __launch_bounds__(kJoinThreads) void paged_attention_join_kernel(cons
 template <int D, bool FP8>
 hipError_t launch(const PagedAttnArgs& a, hipStream_t s) {
     const int rows = a.group < 16 ? a.group : 16;
-    const unsigned lds = static_cast<unsigned>(kWaves * rows * (D + 4) * 4);
+    constexpr unsigned kKeys = kWaves * KvTile<D, FP8>::kBytes;
+    const unsigned sums = static_cast<unsigned>(kWaves * rows * (D + 4) * 4), lds = kKeys > sums ? kKeys : sums;
     const unsigned items = static_cast<unsigned>(a.requests) * static_cast<unsigned>(a.kv_heads * a.head_tiles);
     if (a.aim == 0) {
         paged_attention_kernel<D, FP8, false><<<items, 64 * kWaves, lds, s>>>(a);
@@ -489,22 +528,24 @@ hipError_t launch(const PagedAttnArgs& a, hipStream_t s) {
 
 }  // namespace
 
-// Items are cut where the longest may pass 512 tokens.  Measured at 8 kv heads of 128 dims (us, whole
-// | cut): one request of 256 tokens 5.8 | 9.2, 512 8.0 | 9.3, 1024 13.0 | 9.6, 2048 24 | 10.7; 64 uneven
-// requests of up to 512 tokens 15 | 19, 1024 27 | 27, 2048 46 | 38, 8191 159 | 122.  Beyond 4096 items
-// the items alone are 4 rounds of what the chip holds.
+// Items are cut where the longest may pass 176 KB of keys (704 tokens of 256 bytes) or 1024 tokens.
+// Measured at 8 kv heads (us, whole | cut), one request of 256-byte rows: 400 tokens 7.4 | 10.0,
+// 640 7.5 | 8.7, 777 9.3 | 9.0, 1024 10.5 | 9.0; 64 uneven ones of up to 640 tokens 16 | 20, 1280 29 | 28;
+// 512-byte rows, 640 tokens: 19.6 | 12.4; 64-byte rows, 1024 tokens: 8.9 | 9.1.  Beyond 4096 items the
+// items alone are several rounds of what the chip holds.
 // 1024 pieces, 4 a CU: 512 lost up to 9% (the last ones leave CUs idle), 2048 up to 7% where there are
 // few kv heads and heads of 256 dims (beginnings and ends of pieces), and gained at most 4% elsewhere.
 // A piece has at least a tile a wave.
-void plan_paged_attention(PagedAttnArgs* a, int max_len) {
-    constexpr int kWhole = 512, kMaxItems = 4096, kPieces = 1024;
+void plan_paged_attention(PagedAttnArgs* a, int row_bytes, int max_len) {
+    constexpr int kWholeBytes = 176 << 10, kWholeTokens = 1024, kMaxItems = 4096, kPieces = 1024;
     int64_t reach = static_cast<int64_t>(a->max_pages) * a->page_size;
     const int64_t tiles = a->requests * (reach / 32 + 1);
     if (max_len > 0 && max_len < reach) reach = max_len;
     if (a->window > 0 && a->window < reach) reach = a->window;
     const int64_t items = static_cast<int64_t>(a->requests) * a->kv_heads * a->head_tiles;
+    const bool whole = reach <= kWholeTokens && reach * row_bytes <= kWholeBytes;
     a->least = kWaves;
-    a->aim = reach <= kWhole || items > kMaxItems || tiles >= (int64_t(1) << 31) ? 0 : kPieces;
+    a->aim = whole || items > kMaxItems || tiles >= (int64_t(1) << 31) ? 0 : kPieces;
 }
 
 hipError_t launch_paged_attention(const PagedAttnArgs& a, int head_dim, bool fp8, hipStream_t s) {

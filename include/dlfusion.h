@@ -471,9 +471,9 @@ typedef struct {
                                  * kv head h / (heads / kv_heads) */
     int32_t max_pages;          /* columns of block_table */
     int32_t window;             /* 0, or the last tokens that a request attends to */
-    int32_t max_len;            /* 0, or an upper bound of lens known to the host: up to 512 the
-                                 * requests are not cut into pieces, which saves a launch and the
-                                 * workspace.  A wrong one costs time only */
+    int32_t max_len;            /* 0, or an upper bound of lens known to the host: where no
+                                 * request can be long none is cut into pieces, which saves a launch
+                                 * and the workspace.  A wrong one costs time only */
     int64_t q_stride;           /* elements between two requests' queries, a multiple of 8 */
     float softmax_scale;
 } dlf_paged_attn_desc;
