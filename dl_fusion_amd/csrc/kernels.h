@@ -230,6 +230,7 @@ struct LoraArgs {
     const uint16_t* base;       // [m][n], rows base_stride apart, or nullptr
     uint16_t* out;              // [m][n], rows out_stride apart
     float* h;                   // workspace: [parts][m][rank] partial sums of x A^T
+    uint16_t* nowhere;          // and 1 KB after them
     int64_t x_stride, base_stride, out_stride;
     int m, n, k, rank, adapters, requests;
     int parts;                  // k slices of the first product (lora_parts)

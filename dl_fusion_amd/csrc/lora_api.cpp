@@ -50,9 +50,11 @@ dlf_status check_lora_desc(const dlf_lora_desc* d, dlf::LoraArgs* a) {
     return ok();
 }
 
-size_t lora_ws_bytes(const dlf::LoraArgs& a) {
+size_t lora_h_bytes(const dlf::LoraArgs& a) {
     return static_cast<size_t>(a.parts) * static_cast<size_t>(a.m) * static_cast<size_t>(a.rank) * 4;
 }
+
+size_t lora_ws_bytes(const dlf::LoraArgs& a) { return a.m > 0 ? lora_h_bytes(a) + 1024 : 0; }
 
 }  // namespace
 
@@ -103,6 +105,7 @@ extern "C" dlf_status dlf_lora_add(const dlf_lora_desc* d, const void* x, const 
     a.base = static_cast<const uint16_t*>(base);
     a.out = static_cast<uint16_t*>(out);
     a.h = static_cast<float*>(workspace);
+    a.nowhere = static_cast<uint16_t*>(workspace) + lora_h_bytes(a) / 2;
     const hipError_t e = dlf::launch_lora(a, static_cast<hipStream_t>(stream));
     if (e != hipSuccess) return fail(DLF_ERR_HIP, "dlf_lora_add: %s", hipGetErrorString(e));
     return ok();

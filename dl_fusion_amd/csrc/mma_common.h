@@ -85,8 +85,11 @@ __device__ __forceinline__ void load_lds16_buf(__amdgpu_buffer_rsrc_t r, uint32_
                                              0, 0, 0);
 }
 
-// The same for data that is read once: non-temporal (cache-policy bit 1).  Where every load covers
+// Both for data that is read once: non-temporal (cache-policy bit 1).  Where every load covers
 // whole 128-byte lines, 6.8 TB/s against 6.0; loads of parts of lines lose by it.
+__device__ __forceinline__ void load_lds16_stream(const void* g, uint8_t* lds_wave_base) {
+    __builtin_amdgcn_global_load_lds(g, (__attribute__((address_space(3))) void*)(lds_wave_base), 16, 0, 2);
+}
 __device__ __forceinline__ void load_lds16_stream(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint8_t* lds_wave_base) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)(lds_wave_base), 16, voff,
                                              0, 0, 2);

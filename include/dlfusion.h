@@ -551,7 +551,9 @@ dlf_status dlf_lora_workspace_bytes(const dlf_lora_desc *d, size_t *bytes);
  *   base      device bf16 [m][n], rows base_stride apart, or NULL (= 0)
  *   out       device bf16 [m][n], rows out_stride apart: either base itself with
  *             its stride, or (else DLF_ERR_ALIAS) no overlap with any input
- *   workspace device, 16-byte aligned, as for dlf_paged_attention
+ *   workspace device, 16-byte aligned, at least dlf_lora_workspace_bytes(d)
+ *             bytes, overlapping no operand.  Scratch: calls that share one on
+ *             overlapping streams race
  * UNSUPPORTED: n, k, rank or a stride not a multiple of 8, rank above 128,
  * another dtype, m above 2^24, n or k above 2^23. */
 dlf_status dlf_lora_add(const dlf_lora_desc *d, const void *x, const void *a, const void *b,

@@ -216,3 +216,27 @@ def test_graph_replays():
         ref, tol = definition(s, s["ids"])
         assert ((out.cpu().double() - ref).abs() <= tol).all()
         assert torch.equal(out.cpu(), add(s))
+
+
+@pytest.mark.parametrize("m", [1, 16, 17])
+@pytest.mark.parametrize("k", [8, 56, 8192, 8200])
+@pytest.mark.parametrize("rank", [8, 24, 32, 40])
+def test_few_rows(m, k, rank):
+    """Around the sizes at which one launch does both products."""
+    print(f"adapters m={m} k={k} rank={rank}", flush=True)
+    check(make(m, 328, k, rank, 4, mixed(m, 4)))
+
+
+@pytest.mark.parametrize("rank", [16, 72, 120])
+@pytest.mark.parametrize("n,k", [(40, 136), (1000, 520), (4096, 264)])
+def test_many_rows_of_one_adapter(n, k, rank):
+    print(f"adapters many rows n={n} k={k} rank={rank}", flush=True)
+    check(make(333, n, k, rank, 2, torch.arange(333) // 200))
+    check(make(333, n, k, rank, 2, torch.arange(333) // 200, base=False, more=(8, 0, 16)))
+
+
+@pytest.mark.parametrize("m", [256, 400])
+def test_every_row_its_own_adapter(m):
+    print(f"adapters m={m} all different", flush=True)
+    check(make(m, 128, 128, 16, 64, mixed(m, 64)))
+    check(make(m, 128, 128, 64, m, torch.arange(m)))
