@@ -371,15 +371,17 @@ def dlf_ffn_fused_noalloc(desc, x, w1_packed, b1, w2_packed, b2, residual, y, st
 
 def _rows(t, rank):
     """(device pointer, elements between rows) of a torch tensor whose dimensions after the first
-    are contiguous: [rows][...] with `rank` dimensions; the first may have any stride."""
+    are contiguous: [rows][...] with `rank` dimensions, 2 or 3; the first may have any stride."""
     shape, strides = t.shape, t.stride()
-    if len(shape) != rank:
-        raise ValueError(f"a tensor of {rank} dimensions is needed, got {len(shape)}")
-    width = 1
-    for n, st in zip(reversed(shape[1:]), reversed(strides[1:])):
-        if n != 1 and st != width:
+    if len(strides) != rank:
+        raise ValueError(f"a tensor of {rank} dimensions is needed, got {len(strides)}")
+    width = shape[-1]
+    if strides[-1] != 1 and width != 1:
+        raise ValueError("the dimensions after the first must be contiguous")
+    if rank == 3:
+        if strides[1] != width and shape[1] != 1:
             raise ValueError("the dimensions after the first must be contiguous")
-        width *= n
+        width *= shape[1]
     return t.data_ptr(), strides[0] if shape[0] > 1 else width
 
 
