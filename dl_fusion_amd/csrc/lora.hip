@@ -2,11 +2,11 @@
 //     out[i] = base[i] + scale[a] (x[i] A_a^T) B_a^T,   a the adapter of row i.
 //
 // The second product needs the first one's sum over all of k: h = x A^T in fp32 goes through a workspace
-// (m x rank, small beside x and out) from one kernel to the next; for a few rows one kernel does both.
+// (m x rank, small beside x and out) from one kernel to the next; for a small batch one kernel does both.
 // 2 m rank (k + n) flops over x, base, out and the used adapters' weights: at rank 64 about 60 flops a
 // byte, so both are bound by what they read and, where that is little, by the chain of a workgroup's
 // start (ids, rows, operands).  8192 rows of 4096 at rank 64, 8 adapters: 58 us for 210 MB, 3.6 TB/s;
-// 96 rows of 64 adapters at rank 16: 17.5 us for 15 MB; one row at rank 8: 7.6 us.
+// 96 rows of 64 adapters at rank 16: 15 us for 15 MB; one row at rank 8: 7.0 us.
 //
 // Rows of one adapter are gathered per tile of 64 rows: a wave holds the tile's adapters one a lane,
 // and a ballot gives the rows that share the first one left, so any order of rows is served, a run of
@@ -62,6 +62,28 @@ __device__ __forceinline__ void for_each_adapter(int id, uint64_t there, int slo
         there &= ~same;
         if (turn == slot) f(cur, same);
         turn = turn + 1 == slots ? 0 : turn + 1;
+    }
+}
+
+// The same by at most 16 rows of an adapter at a time, each such group a turn of its own.
+template <class Fn>
+__device__ __forceinline__ void for_each_16(int id, int lane, uint64_t there, int slot, int slots, Fn&& f) {
+    const int rows = __popcll(there);       // the first lanes
+    int before = 0;                         // rows before this one that share its adapter
+    auto count = [&](auto first_c, auto last_c) {
+#pragma unroll
+        for (int j = decltype(first_c)::value; j < decltype(last_c)::value; ++j)
+            before += lane > j && id == __builtin_amdgcn_readlane(id, j);
+    };
+    if (rows > 1) count(std::integral_constant<int, 0>{}, std::integral_constant<int, 15>{});
+    if (rows > 16) count(std::integral_constant<int, 15>{}, std::integral_constant<int, 63>{});
+    uint64_t firsts = __ballot((before & 15) == 0) & there;
+    for (int turn = 0; firsts; ++turn, firsts &= firsts - 1) {
+        if (turn < slot) continue;
+        const int l = __builtin_ctzll(firsts);
+        const int cur = __builtin_amdgcn_readlane(id, l), from = __builtin_amdgcn_readlane(before, l);
+        f(cur, __ballot(id == cur && before >= from && before < from + 16) & there);
+        slot += slots;
     }
 }
 
@@ -367,23 +389,27 @@ __global__ __launch_bounds__(64 * kWaves, 2) void lora_shrink_kernel(const LoraA
 // the output's own.
 // More than 16 rows: a wave has 16 of them and all columns; B and base go through a ring of blocks, as the
 // first product's slices do.  Up to 16 rows: the waves take the blocks in turns, a few at a time each.
-// SELF: for at most 16 rows, the workgroup computes the adapter's h by itself: every range of the columns
-// reads A again, from L2, which saves a launch and h's way through memory.  Else h comes from the workspace.
+// SELF: for a small batch, 16 rows of an adapter at a time: the workgroup computes the adapter's h by itself.
+// Every range of the columns reads A again, from L2, which saves a launch and h's way through memory.  Else h
+// comes from the workspace.
 template <int RF, bool SELF>
 struct OutLds {
     static constexpr int kSteps = (RF + 1) / 2;             // of 32 ranks
     static constexpr int kCols = kSteps == 4 ? 32 : 64;     // of a block
-    static constexpr int kB = kCols * kSteps * 64;          // bytes of a block of B
+    static constexpr int kB = kCols * (SELF ? 16 * RF : 32 * kSteps) * 2;   // bytes of a block of B
     static constexpr int kBase = kTileRows * kCols * 2;     // and of base
     static constexpr int kDepth = kSteps == 2 ? 4 : 5;
     static constexpr int kOwn = 16 * kCols * 4;             // a wave's 16 rows of products, fp32
     static constexpr int kOwnBlocks = kSteps == 1 && !SELF ? 4 : 2;  // blocks that a wave has of its own at a time
     static constexpr int kMany = kDepth * (kB + kBase), kFew = kWaves * kOwnBlocks * kB;
-    static constexpr int kSelfDepth = RF == 1 ? 6 : 4;      // slices of multiply_alone()
+    static constexpr int kSelfDepth = RF == 1 ? 3 : 4;      // slices of multiply_alone()
     static constexpr int kPitch = 32 * kSteps + 8;          // bf16 values of a row of h: 16 rows in different banks
     static constexpr int kH = SELF ? 2 * 16 * kPitch * 2 : 0;
-    static constexpr int kRings = SELF ? kFew + kWaves * kSelfDepth * (1 + RF) * 2048 : kMany > kFew ? kMany : kFew;
-    static constexpr int kBytes = kWaves * kOwn + kH + kRings;
+    // SELF: the first product's ring is free when products come, and holds them
+    static constexpr int kSelf = kWaves * kSelfDepth * (1 + RF) * 2048;
+    static constexpr int kRings = SELF ? kFew : kMany > kFew ? kMany : kFew;
+    static constexpr int kBytes = kH + kRings + (SELF ? kSelf : kWaves * kOwn);
+    static_assert(kWaves * kOwn <= kSelf, "own");
 };
 
 template <int RF, bool SELF>
@@ -400,9 +426,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void lora_out_kernel(const LoraArgs
     const int cb0 = static_cast<int>(static_cast<int64_t>(blocks) * blockIdx.y / gridDim.y);
     const int cb1 = static_cast<int>(static_cast<int64_t>(blocks) * (blockIdx.y + 1) / gridDim.y);
     const int id = adapter_of(p, row0 + lane);
-    uint8_t* const own = lds + wave * L::kOwn;
-    uint16_t* const h_s = reinterpret_cast<uint16_t*>(lds + kWaves * L::kOwn);      // SELF: hi, then lo
-    uint8_t* const rings = lds + kWaves * L::kOwn + L::kH;
+    uint16_t* const h_s = reinterpret_cast<uint16_t*>(lds);     // SELF: hi, then lo
+    uint8_t* const rings = lds + L::kH;
+    uint8_t* const own = lds + L::kH + L::kRings + wave * L::kOwn;
 
     // what a lane moves of 16 rows: row o_row (+ 16 / U for the second load), 8 columns
     const int o_row = lane / (C / 8), o_col = 8 * (lane % (C / 8));
@@ -554,7 +580,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void lora_out_kernel(const LoraArgs
         fetch(cb0 + wave);      // on its way while h is made
         u32x4_t hi[RS], lo[RS];
         if constexpr (SELF) {
-            multiply_alone<RF, L::kSelfDepth>(p, rings + L::kFew, wave, lane, row0, place, cur, 0, p.k, [&](int c, int, f32x4_t v) {
+            multiply_alone<RF, L::kSelfDepth>(p, lds + L::kH + L::kRings, wave, lane, row0, place, cur, 0, p.k, [&](int c, int, f32x4_t v) {
                 uint32_t h[2], l[2];
                 split(v, scale, h, l);
                 const int at = li * L::kPitch + 16 * c + 4 * g;
@@ -655,7 +681,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void lora_out_kernel(const LoraArgs
     };
 
     const int slot = static_cast<int>(gridDim.z - 1 - blockIdx.z);      // second passes first: they are few
-    for_each_adapter(id, __ballot(row0 + lane < p.m), slot, static_cast<int>(gridDim.z), [&](int cur, uint64_t same) {
+    auto pass = [&](int cur, uint64_t same) {
         if (cur < 0) {      // rows without an adapter: base, or zeros
             const int count = __popcll(same), place = nth_lane(same, lane);
             for (int at0 = 0; at0 < count; at0 += 16 / U) {
@@ -671,7 +697,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void lora_out_kernel(const LoraArgs
         } else if constexpr (!SELF) {
             many(cur, same);
         }
-    });
+    };
+    const uint64_t there = __ballot(row0 + lane < p.m);
+    if constexpr (SELF) for_each_16(id, lane, there, slot, static_cast<int>(gridDim.z), pass);
+    else for_each_adapter(id, there, slot, static_cast<int>(gridDim.z), pass);
 }
 
 int tiles_of(int m) { return (m + kTileRows - 1) / kTileRows; }
@@ -682,10 +711,13 @@ int passes_of(int m, int adapters) {
     return rows < adapters + 1 ? rows : adapters + 1;
 }
 
-// Passes that get workgroups of their own when the work is split: in up to 4 tiles (a decode batch) any row
-// may have an adapter of its own; more rows are made of runs.  256 rows of 64 adapters, rank 16: 24 us with
-// all passes, 37 with one; 257 rows in runs of 32: 15 us with one, 75 with all (k is then hardly split).
-int expected_passes(int m, int adapters) { return tiles_of(m) <= 4 ? passes_of(m, adapters) : 1; }
+// Passes that get workgroups of their own when the work is split.  In up to 4 tiles (a decode batch) any
+// row may have an adapter of its own, or all rows one; more rows are made of runs.  256 rows of 64 adapters
+// at rank 64, all different | all one (us): with 4 passes 58 | 22, 16 46 | 29, 64 47 | 87, so 64 in all tiles.
+int expected_passes(int m, int adapters) {
+    const int most = passes_of(m, adapters), tiles = tiles_of(m);
+    return tiles > 4 ? 1 : most < kTileRows / tiles ? most : kTileRows / tiles;
+}
 
 // Passes of a tile side by side, where `others` workgroups share each: as many as it can have, while that
 // leaves CUs idle, and in a large batch a second one for the tiles that two runs share.
@@ -724,11 +756,14 @@ int lora_parts(int m, int k, int adapters) {
 
 hipError_t launch_lora(const LoraArgs& a, hipStream_t s) {
     const int blocks = (a.n + 63) / 64;
-    // One launch (us, against two): one row at k = 4096, rank 8 7.5 | 11.5 as called and 7.4 | 9.0 in a graph,
-    // 16 rows at rank 32 10.6 | 13.5; at k = 11008 13.6 | 11.6: a workgroup alone reads A.
-    if (a.m <= 16 && a.rank <= 32 && a.k <= 8192) {
-        const int passes = passes_of(a.m, a.adapters);
-        const int ranges = at_most(256 / passes, (blocks + kWaves - 1) / kWaves);
+    // One launch (us as called, against two) at n = k = 4096: one row at rank 8 7.0 | 9.4, 16 rows of 16 adapters
+    // at rank 32 10 | 13; 96 rows at rank 16, of 64 adapters 14.7 | 18.6, of one 15 | 14.4; 256 rows of one run
+    // 10.7 | 14.7, of 64 adapters 20.6 | 24.  A workgroup alone reads its A: k = 8192 18 | 16, 11008 12 | 9.3 (one row).
+    if (a.m <= 256 && a.rank <= 32 && a.k <= 6144) {
+        const int groups = ((a.m < kTileRows ? a.m : kTileRows) + 15) / 16, most = passes_of(a.m, a.adapters);
+        const int passes = most > groups ? most : groups;
+        // rank 16 leaves room for two workgroups a CU
+        const int ranges = at_most((a.rank <= 16 ? kWorkgroups : 256) / (passes * tiles_of(a.m)), (blocks + kWaves - 1) / kWaves);
         if (a.rank <= 16) launch_out<1, true>(a, passes, ranges, s);
         else launch_out<2, true>(a, passes, ranges, s);
         return hipGetLastError();

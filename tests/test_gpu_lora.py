@@ -240,3 +240,16 @@ def test_every_row_its_own_adapter(m):
     print(f"adapters m={m} all different", flush=True)
     check(make(m, 128, 128, 16, 64, mixed(m, 64)))
     check(make(m, 128, 128, 64, m, torch.arange(m)))
+
+
+@pytest.mark.parametrize("rank", [8, 32, 40])
+@pytest.mark.parametrize("k", [136, 6144, 6152])
+def test_groups_of_one_adapter_in_a_small_batch(k, rank):
+    """Groups of 15 to 48 rows among single ones, in any order, around the sizes at which one launch does both."""
+    g = torch.Generator().manual_seed(3)
+    ids = torch.cat([torch.full((n,), i) for i, n in enumerate([15, 16, 17, 33, 48, 1, 1, 5])] + [torch.full((9,), -1)])
+    print(f"adapters groups k={k} rank={rank}", flush=True)
+    check(make(ids.numel(), 200, k, rank, 8, ids))
+    check(make(ids.numel(), 200, k, rank, 8, ids[torch.randperm(ids.numel(), generator=g)]))
+    check(make(256, 200, k, rank, 1, torch.zeros(256)))
+    check(make(257, 200, k, rank, 70, torch.arange(257) % 70))
