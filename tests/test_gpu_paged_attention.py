@@ -298,3 +298,30 @@ def test_repeats_give_the_same_bits():
     for _ in range(3):
         b, lb = attend(s, 0.1, dev=dev)
         assert torch.equal(a, b) and torch.equal(la, lb)
+
+
+def test_offsets_beyond_32_bits():
+    """The same pages at the far end of caches of more than 4 GB give the same bits."""
+    import dl_fusion_amd as dl
+    s = make([700, 33, 0, 1500], 16, 8, 128, 16)
+    cache, dev = device(s)
+    pages = (1 << 32) // (8 * 16 * 128 * 2) + 1000
+    if torch.cuda.mem_get_info()[0] < 2 * pages * 8 * 16 * 128 * 2 + (1 << 30):
+        pytest.skip("not enough memory")
+    print("attention cache of 4.03 GB each", flush=True)
+    far = dict(dev, k=torch.empty(pages, 8, 16, 128, dtype=torch.bfloat16, device="cuda"),
+               v=torch.empty(pages, 8, 16, 128, dtype=torch.bfloat16, device="cuda"))
+    shift = pages - s["pages"]
+    far["k"][shift:], far["v"][shift:] = dev["k"], dev["v"]
+    far["table"] = torch.where((dev["table"] >= 0) & (dev["table"] < s["pages"]), dev["table"] + shift, dev["table"])
+    near = attend(s, 0.09, dev=(cache, dev))
+    big = dl.kv_cache_desc(pages, 8, 16, 128)
+    got = attend(s, 0.09, dev=(big, far))
+    assert torch.equal(near[0], got[0]) and torch.equal(near[1], got[1])
+    # and the store reaches there
+    x = torch.randn(3, 8, 128, device="cuda").to(torch.bfloat16)
+    slots = torch.tensor([pages * 16 - 1, -1, pages * 16 - 18], device="cuda")
+    dl.dlf_paged_store(big, x, -x, slots, far["k"], far["v"])
+    torch.cuda.synchronize()
+    assert torch.equal(far["k"][-1, :, 15], x[0]) and torch.equal(far["v"][-1, :, 15], -x[0])
+    assert torch.equal(far["k"][-2, :, 14], x[2]) and torch.equal(far["v"][-2, :, 14], -x[2])
