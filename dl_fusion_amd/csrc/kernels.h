@@ -235,7 +235,7 @@ struct LoraArgs {
     int m, n, k, rank, adapters, requests;
     int parts;                  // k slices of the first product (lora_parts)
 };
-int lora_parts(int m, int k, int adapters);
+int lora_parts(int m, int k, int rank, int adapters);
 hipError_t launch_lora(const LoraArgs& args, hipStream_t stream);
 
 // Shader-clock probe: workgroups x 4 waves of back-to-back bf16 MFMAs; stamps[4 b + 0..3] =

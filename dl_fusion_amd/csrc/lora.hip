@@ -741,17 +741,23 @@ void launch_shrink(const LoraArgs& a, hipStream_t s) {
     lora_shrink_kernel<RF><<<grid, 64 * kWaves, kRingBytes, s>>>(a);
 }
 
+// Multiples of 16 tiles, once some CUs get a second workgroup, run slower than their neighbours, which an
+// empty tile mends by making the number odd (measured; the cause is not known): 4096 rows at rank 64, n = 4096 |
+// 11008, 41 us | 68, without it 50 | 83.  Up to one workgroup a CU it costs: 16384 rows 127, without 122.
 template <int RF, bool SELF>
 void launch_out(const LoraArgs& a, int slots, int ranges, hipStream_t s) {
-    const dim3 grid(static_cast<unsigned>(tiles_of(a.m)), static_cast<unsigned>(ranges), static_cast<unsigned>(slots));
+    const int tiles = tiles_of(a.m), empty = tiles % 16 == 0 && tiles * ranges > 256 ? 1 : 0;
+    const dim3 grid(static_cast<unsigned>(tiles + empty), static_cast<unsigned>(ranges), static_cast<unsigned>(slots));
     lora_out_kernel<RF, SELF><<<grid, 64 * kWaves, OutLds<RF, SELF>::kBytes, s>>>(a);
 }
 
 }  // namespace
 
-int lora_parts(int m, int k, int adapters) {
-    const int most = (k + 255) / 256;
-    return at_most(kWorkgroups / at_most(tiles_of(m) * expected_passes(m, adapters), kWorkgroups), most < 16 ? most : 16);
+// Every range of the second kernel reads all parts of h, so that many of them cost.  2048 rows at rank 64 (us):
+// 4 parts 36, 8 39, 12 46; 512 rows 23.0, 21.0, 16 parts 23.1; 2048 rows at rank 16 31.3, 29.8, 33.6.
+int lora_parts(int m, int k, int rank, int adapters) {
+    const int most = (k + 255) / 256, cap = rank <= 32 || tiles_of(m) <= 8 ? 8 : 4;
+    return at_most(kWorkgroups / at_most(tiles_of(m) * expected_passes(m, adapters), kWorkgroups), most < cap ? most : cap);
 }
 
 hipError_t launch_lora(const LoraArgs& a, hipStream_t s) {

@@ -46,7 +46,7 @@ dlf_status check_lora_desc(const dlf_lora_desc* d, dlf::LoraArgs* a) {
     a->rank = d->rank;
     a->adapters = d->adapters;
     a->requests = d->requests;
-    a->parts = d->m > 0 ? dlf::lora_parts(a->m, a->k, a->adapters) : 1;
+    a->parts = d->m > 0 ? dlf::lora_parts(a->m, a->k, a->rank, a->adapters) : 1;
     return ok();
 }
 
