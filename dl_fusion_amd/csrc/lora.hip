@@ -780,8 +780,14 @@ hipError_t launch_lora(const LoraArgs& a, hipStream_t s) {
     else launch_shrink<8>(a, s);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const int ranges = at_most(kWorkgroups / at_most(tiles_of(a.m) * expected_passes(a.m, a.adapters), kWorkgroups),
-                               (blocks + kWaves - 1) / kWaves);
+    const int split = at_most(tiles_of(a.m) * expected_passes(a.m, a.adapters), kWorkgroups);
+    // Ranges of 4 blocks give each wave one where few rows share an adapter.  Shorter ones pay up to one workgroup
+    // a CU, counting a second pass in all but small batches: at rank 64 (us, against 4 blocks) 52 rows, n = 4096
+    // 15.2 | 17.4, 1024 rows, n = 1024 19.6 | 21.5, but 300 rows in runs of 40 21.6 | 21.0 (without that pass 23.9).
+    // Up to kWorkgroups as well: 512 rows, n = 4096 22.6 | 21.0, 2097 rows, n = 1608 30 | 27.
+    const int of_4 = (blocks + kWaves - 1) / kWaves;
+    const int one_a_cu = at_most(256 / (tiles_of(a.m) > 4 ? 2 * split : split), blocks);
+    const int ranges = at_most(kWorkgroups / split, of_4 > one_a_cu ? of_4 : one_a_cu);
     const int slots = slots_of(a.m, a.adapters, ranges);
     if (a.rank <= 32) launch_out<2, false>(a, slots, ranges, s);
     else if (a.rank <= 64) launch_out<4, false>(a, slots, ranges, s);
