@@ -762,12 +762,14 @@ int lora_parts(int m, int k, int rank, int adapters) {
 
 hipError_t launch_lora(const LoraArgs& a, hipStream_t s) {
     const int blocks = (a.n + 63) / 64;
-    // One launch (us as called, against two) at n = k = 4096: one row at rank 8 7.0 | 9.4, 16 rows of 16 adapters
-    // at rank 32 10 | 13; 96 rows at rank 16, of 64 adapters 14.7 | 18.6, of one 15 | 14.4; 256 rows of one run
-    // 10.7 | 14.7, of 64 adapters 20.6 | 24.  A workgroup alone reads its A: k = 8192 18 | 16, 11008 12 | 9.3 (one row).
+    // One launch (us as called, against two) at n = k = 4096: one row at rank 8 7.8 | 11.0, 16 rows of 16 adapters
+    // at rank 32 9.3 | 12.8; 96 rows at rank 16, of 64 adapters 14.7 | 18.6, of one 10.1 | 12.4; 256 rows of one run
+    // 10.6 | 13.5, of 64 adapters 21.0 | 24.7.  A workgroup alone reads its A: one row at rank 32, k = 6144 9.8 | 11.0,
+    // 8192 11.4 | 11.2, 11008 13.4 | 10.6 (without the call 9.4 | 8.4, 11.4 | 8.6, 13.6 | 8.9).
     if (a.m <= 256 && a.rank <= 32 && a.k <= 6144) {
-        const int groups = ((a.m < kTileRows ? a.m : kTileRows) + 15) / 16, most = passes_of(a.m, a.adapters);
-        const int passes = most > groups ? most : groups;
+        // groups of 16 rows that a tile can have, at most: one begun for each adapter, the others full
+        const int most = passes_of(a.m, a.adapters);
+        const int passes = most + ((a.m < kTileRows ? a.m : kTileRows) - most) / 16;
         // rank 16 leaves room for two workgroups a CU
         const int ranges = at_most((a.rank <= 16 ? kWorkgroups : 256) / (passes * tiles_of(a.m)), (blocks + kWaves - 1) / kWaves);
         if (a.rank <= 16) launch_out<1, true>(a, passes, ranges, s);
