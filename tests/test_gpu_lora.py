@@ -253,3 +253,28 @@ def test_groups_of_one_adapter_in_a_small_batch(k, rank):
     check(make(ids.numel(), 200, k, rank, 8, ids[torch.randperm(ids.numel(), generator=g)]))
     check(make(256, 200, k, rank, 1, torch.zeros(256)))
     check(make(257, 200, k, rank, 70, torch.arange(257) % 70))
+
+
+# Batches whose number of tiles is a multiple of 16 and one off it, with two workgroups a CU and one; runs
+# that end inside a tile, at its end, and longer ones
+@pytest.mark.parametrize("run", [64, 100, 5000])
+@pytest.mark.parametrize("m,n", [(1024, 2056), (1025, 2056), (1024, 968), (960, 72), (2048, 1032)])
+@pytest.mark.parametrize("rank", [16, 128])
+def test_tiles_and_ranges(rank, m, n, run):
+    ids = (torch.arange(m) // run) % 4 - 1
+    check(make(m, n, 136, rank, 3, ids, seed=13))
+
+
+# Short ranges of columns: few tiles, widths of one block and a few, all rows of one adapter or of several
+@pytest.mark.parametrize("n", [8, 64, 200, 1544])
+@pytest.mark.parametrize("m,adapters", [(1, 1), (18, 1), (64, 2), (257, 1), (330, 3)])
+def test_short_ranges(m, adapters, n):
+    check(make(m, n, 520, 64, adapters, mixed(m, adapters), seed=14))
+
+
+# One row without an adapter among 63 of one, and pools whose groups of 16 rows end anywhere
+@pytest.mark.parametrize("adapters", [1, 2, 5])
+@pytest.mark.parametrize("m", [33, 49, 64, 200])
+def test_groups_of_few_adapters(m, adapters):
+    for ids in (mixed(m, adapters), torch.where(torch.arange(m) % 64 == 7, -1, 0), torch.arange(m) % (adapters + 1) - 1):
+        check(make(m, 264, 264, 24, adapters, ids, seed=15))
