@@ -433,7 +433,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void lora_out_kernel(const LoraArgs
     // what a lane moves of 16 rows: row o_row (+ 16 / U for the second load), 8 columns
     const int o_row = lane / (C / 8), o_col = 8 * (lane % (C / 8));
     const int block_bytes = C * p.rank * 2, block_kb = (block_bytes + 1023) / 1024;
-    // KB j of block cb; what lies past the adapter's end, and KB past the block's, come as zeros
+    // KB j of block cb; what lies past the adapter's end comes as zeros, and KB past the block's too: many() loads
+    // those, so that its loads are as many at every rank, few() leaves them as they are
     auto load_b = [&](__amdgpu_buffer_rsrc_t br, int cb, int j, uint8_t* to) {
         const uint32_t q = static_cast<uint32_t>(64 * j + lane);
         const uint32_t at = static_cast<uint32_t>(cb) * static_cast<uint32_t>(block_bytes) + 16 * (q ^ (q >> 4 & 15));
@@ -498,8 +499,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void lora_out_kernel(const LoraArgs
             const uint32_t q = static_cast<uint32_t>((16 * i + li) * (p.rank / 8) + 4 * s + g);
             b_at[s][i] = 16 * (q ^ (q >> 4 & 15));
         }
-    // in the last 32 ranks, the lanes past the last rank: what they read is another column's
-    const bool past = 32 * (RS - 1) + 8 * g >= p.rank;
+    // The steps of 32 ranks from the smallest rank that comes here on (of 65..128 ranks, the third and the
+    // fourth) may have lanes past the last rank: what these read is another column's or nobody's, and is cleared,
+    // since an infinity or NaN there would not vanish against the zeros of h.
+    constexpr int kWhole = RF == 8 ? 2 : RF == 4 ? 1 : 0;
     // the wave's own LDS: 16-byte chunk c of row r
     auto own_at = [&](int r, int c) {
         return reinterpret_cast<f32x4_t*>(own + 4 * C * r + 16 * (c ^ (C == 64 ? r & 15 : r >> 1 & 7)));
@@ -512,9 +515,13 @@ __global__ __launch_bounds__(64 * kWaves, 2) void lora_out_kernel(const LoraArgs
 #pragma unroll
             for (int i = 0; i < F; ++i) bf[s][i] = *reinterpret_cast<const u32x4_t*>(b + b_at[s][i]);
 #pragma unroll
-        for (int i = 0; i < F; ++i)
+        for (int s = kWhole; s < RS; ++s) {
+            const bool past = 32 * s + 8 * g >= p.rank;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) bf[RS - 1][i][e] = past ? 0u : bf[RS - 1][i][e];
+            for (int i = 0; i < F; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) bf[s][i][e] = past ? 0u : bf[s][i][e];
+        }
         f32x4_t y[F];
 #pragma unroll
         for (int i = 0; i < F; ++i) y[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};

@@ -278,3 +278,33 @@ def test_short_ranges(m, adapters, n):
 def test_groups_of_few_adapters(m, adapters):
     for ids in (mixed(m, adapters), torch.where(torch.arange(m) % 64 == 7, -1, 0), torch.arange(m) % (adapters + 1) - 1):
         check(make(m, 264, 264, 24, adapters, ids, seed=15))
+
+
+def few_and_many(m=90):
+    """Adapter 0 on 5 rows of a tile, adapter 1 on 40 of one, adapter 2 on the rest, a row without any."""
+    return torch.cat([torch.zeros(5), torch.full((40,), 1.0), torch.full((m - 46,), 2.0), torch.tensor([-1.0])]).long()
+
+
+# every rank that is admitted, up to 16 rows of an adapter and more
+@pytest.mark.parametrize("rank", range(8, 136, 8))
+def test_every_rank(rank):
+    print(f"adapters rank={rank}", flush=True)
+    ids = few_and_many()
+    check(make(ids.numel(), 328, 264, rank, 3, ids))
+    check(make(13, 328, 264, rank, 3, mixed(13, 3), base=False))
+    check(make(300, 328, 264, rank, 3, torch.arange(300) // 110))
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("rank", [8, 24, 40, 56, 72, 80, 88, 96, 104, 120])
+def test_a_weight_not_finite_stays_in_its_column(rank, bad):
+    """Outputs of a column depend on that row of B alone."""
+    cols = [0, 1, 17, 32, 63, 100, 135]
+    for ids in (few_and_many(), mixed(9, 3)):
+        s = make(ids.numel(), 136, 264, rank, 3, ids)
+        s["b"][:, cols] = bad
+        print(f"adapters rank={rank} bad={bad}", flush=True)
+        got = add(s)
+        ref, tol = definition(s, s["ids"])
+        rest = [c for c in range(136) if c not in cols]
+        assert ((got.double() - ref).abs()[:, rest] <= tol[:, rest]).all()
