@@ -72,6 +72,11 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t){a, b}, bf16x2_t));
 }
 
+// All ones in the halves that are an infinity or NaN.
+__device__ __forceinline__ uint32_t not_finite_bf16x2(uint32_t u) {
+    return ((u & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) | ((u & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
+}
+
 // ReLU of two packed bf16 values: a value with the sign bit set becomes +0 (as a signed
 // 16-bit integer it is negative, so one packed integer max with 0 does both halves).
 // Rounding to nearest keeps the sign, so ReLU after the rounding equals the rounding of ReLU.

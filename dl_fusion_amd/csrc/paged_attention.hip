@@ -20,6 +20,8 @@
 //    tokens gives the 8 tokens of each of its dims: the order of the dims among the lanes is free, since
 //    the result's rows come out in the same order.
 // 16 query rows are computed whatever the group: the rest is zeros and costs nothing that bounds.
+#include <type_traits>
+
 #include "device_common.h"
 #include "kernels.h"
 #include "mma_common.h"
@@ -95,6 +97,10 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t x) {
     x += __builtin_amdgcn_update_dpp(0u, x, 0x143, 0xC, 0xF, false);
     return x;
 }
+
+// Where parts are joined to NaN, the factor of a part's sum o once more.  A part whose maximum is so far below the
+// others' that f is 0 adds nothing, unless its sum is infinite: no probability is 0, so that the infinity stays.
+__device__ __forceinline__ float weight_of(float f, float o) { return f == 0.0f && __builtin_isinf(o) ? 1.0f : f; }
 
 // What a workgroup takes: tiles [tile, end) of request r, for one kv head and tile of its query heads.
 struct Work {
@@ -289,7 +295,9 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : D == 128 ? 3 : 4) void 
                 sc[hh] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, k), qf[s], sc[hh], 0, 0, 0);
             }
     };
-    auto add_values = [&](const Where& w, uint32_t at, Tile& t, const f32x4_t (&sc)[2]) {
+    // EXTENDED: values that are not finite kept apart, as explained at the second pass below
+    auto add_values = [&](auto extended_c, const Where& w, uint32_t at, Tile& t, const f32x4_t (&sc)[2]) {
+        constexpr bool EXTENDED = decltype(extended_c)::value;
         // lane: query qi, tokens tok0 + 16 hh + 4 g + e
         const int tok0 = t16 + static_cast<int>(at);
         float z[8];
@@ -332,7 +340,30 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : D == 128 ? 3 : 4) void 
         l = l * alpha + sum;
         const bf16x8_t pf = __builtin_bit_cast(bf16x8_t, u32x4_t{ph[0], ph[1], ph[2], ph[3]});
         const bf16x8_t pg = __builtin_bit_cast(bf16x8_t, u32x4_t{pl[0], pl[1], pl[2], pl[3]});
+        // EXTENDED: 1 for every token that counts, however little; NaN and the 0 of a score of -inf stay
+        uint32_t pc[4] = {};
+        if constexpr (EXTENDED) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                pc[i] = pack_bf16x2(z[2 * i] > -INFINITY ? 1.0f : pr[2 * i], z[2 * i + 1] > -INFINITY ? 1.0f : pr[2 * i + 1]);
+        }
         auto add = [&](int i, u32x4_t vt) {
+            if constexpr (EXTENDED) {
+                u32x4_t apart;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t bad = not_finite_bf16x2(vt[e]);
+                    apart[e] = vt[e] & bad;
+                    vt[e] &= ~bad;
+                    o[i][e] *= __builtin_isinf(o[i][e]) ? 1.0f : alpha;
+                }
+                const bf16x8_t vf = __builtin_bit_cast(bf16x8_t, vt);
+                o[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pf, o[i], 0, 0, 0);
+                o[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, pg, o[i], 0, 0, 0);
+                o[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, apart),
+                                                               __builtin_bit_cast(bf16x8_t, u32x4_t{pc[0], pc[1], pc[2], pc[3]}), o[i], 0, 0, 0);
+                return;
+            }
             const bf16x8_t vf = __builtin_bit_cast(bf16x8_t, vt);
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[i][e] *= alpha;
@@ -392,7 +423,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : D == 128 ? 3 : 4) void 
             __builtin_amdgcn_sched_barrier(0);      // the tile's reads are done
             fetch_keys(next);
             __builtin_amdgcn_sched_barrier(0);
-            add_values(w, at, t, sc);
+            add_values(std::false_type{}, w, at, t, sc);
             __builtin_amdgcn_sched_barrier(0);
             fetch_values(next, t);
             __builtin_amdgcn_sched_barrier(0);
@@ -401,7 +432,35 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : D == 128 ? 3 : 4) void 
         }
         wait_vmcnt<kValueLoads>();
         scores(sc);
-        add_values(w, at, t, sc);
+        add_values(std::false_type{}, w, at, t, sc);
+    }
+    // A value of infinity has become NaN wherever hi or lo of its probability is 0, lo is below it, or a later
+    // rescaling is by 0; every such mistake is a NaN.  So a wave that has one goes over its tiles once more, in no
+    // hurry, with two products of the finite values and a third of the others by 1: an infinity in the sum, NaN where
+    // both signs meet or a value is NaN.  e4m3 has no infinities.  The look for NaN takes 0.1 to 0.2 us of a call.
+    if constexpr (!FP8) {
+        f32x4_t any{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < kFrag; ++i) any += o[i];
+        if (__builtin_expect(__ballot(__builtin_isnan(any[0] + any[1] + any[2] + any[3]) && qi < nq) != 0, 0)) {
+#pragma unroll
+            for (int i = 0; i < kFrag; ++i) o[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+            m = -INFINITY;
+            l = 0.0f;
+            for (uint32_t i = 0; i < tiles; ++i) {
+                if ((i & 31) == 0) find_runs(i);
+                const Where w = locate(i);
+                Tile t;
+                f32x4_t sc[2];
+                fetch_keys(w);
+                fetch_values(w, t);
+                wait_vmcnt<0>();
+                __builtin_amdgcn_sched_barrier(0);
+                scores(sc);
+                __builtin_amdgcn_sched_barrier(0);      // the tile's reads are done
+                add_values(std::true_type{}, w, 32 * (first + kWaves * i), t, sc);
+            }
+        }
     }
 
     // ---- the waves' results joined through LDS ----
@@ -429,12 +488,21 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 2 : D == 128 ? 3 : 4) void 
         for (int w = 1; w < kWaves; ++w) top = fmaxf(top, m_s[w][row]);
         const float base = top == -INFINITY ? 0.0f : top;
         float x = 0.0f, y = 0.0f, sum = 0.0f;
+        const float* const from = o_s + row * kPad + dim;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
             const float f = __builtin_amdgcn_exp2f(m_s[w][row] - base);
-            x += f * o_s[(w * rows + row) * kPad + dim];
-            y += f * o_s[(w * rows + row) * kPad + dim + 1];
+            x += f * from[w * rows * kPad];
+            y += f * from[w * rows * kPad + 1];
             sum += f * l_s[w][row];
+        }
+        if (__builtin_expect(__builtin_isunordered(x, y), 0)) {
+            x = y = 0.0f;
+            for (int w = 0; w < kWaves; ++w) {
+                const float f = __builtin_amdgcn_exp2f(m_s[w][row] - base), a = from[w * rows * kPad], b = from[w * rows * kPad + 1];
+                x += weight_of(f, a) * a;
+                y += weight_of(f, b) * b;
+            }
         }
         if (CUT && work.pieces > 1) {
             const int64_t at = static_cast<int64_t>(blockIdx.x) * rows + row;
@@ -488,6 +556,16 @@ __global__ __launch_bounds__(kJoinThreads) void paged_attention_join_kernel(cons
         sum += f * ml[1];
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[e] += f * x[e];
+    }
+    if (__builtin_expect(__builtin_isunordered(o[0], o[1]) || __builtin_isunordered(o[2], o[3]), 0)) {
+        o = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int s = down; s < mine; s += kDown) {
+            const int64_t at = place(s);
+            const f32x4_t x = *reinterpret_cast<const f32x4_t*>(p.part_o + at * D + 4 * c);
+            const float f = __builtin_amdgcn_exp2f(p.part_ml[2 * at] - base);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] += weight_of(f, x[e]) * x[e];
+        }
     }
     o_s[down][c] = o;
     if (c == 0) l_s[down] = sum;

@@ -495,7 +495,9 @@ dlf_status dlf_paged_attention_workspace_bytes(const dlf_paged_attn_desc *d, siz
  * probabilities enter the second product as a sum of two bf16 values (2^-17
  * relative), and out is rounded once.  The order of the sums depends on the
  * lengths and the descriptor alone: the same inputs give the same bits.  A NaN
- * in a key or value in range reaches the outputs that use it.
+ * in a key or value in range reaches the outputs that use it, and an infinity
+ * among the values of a dim gives that infinity (NaN where both signs meet),
+ * however small its probability.
  *   q            device bf16 [requests][heads][head_dim], requests q_stride apart
  *   k_cache, v_cache  device, laid out as in dlf_kv_cache_desc
  *   block_table  device [requests][max_pages] int32

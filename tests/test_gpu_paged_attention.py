@@ -325,3 +325,65 @@ def test_offsets_beyond_32_bits():
     torch.cuda.synchronize()
     assert torch.equal(far["k"][-1, :, 15], x[0]) and torch.equal(far["v"][-1, :, 15], -x[0])
     assert torch.equal(far["k"][-2, :, 14], x[2]) and torch.equal(far["v"][-2, :, 14], -x[2])
+
+
+def check_extended(s, scale, window=0):
+    """Infinities and NaN where the definition has them, the bounds elsewhere."""
+    out, lse = attend(s, scale, window)
+    out = out.double()
+    ref, tol, ref_lse, tol_lse = definition(s, scale, window)
+    assert torch.equal(out.isnan(), ref.isnan())
+    wide = ref.isinf()
+    assert torch.equal(out[wide], ref[wide])
+    rest = ref.isfinite()
+    assert ((out - ref).abs()[rest] <= tol[rest]).all()
+    assert ((lse.double() - ref_lse).abs() <= tol_lse).all()
+    return ref
+
+
+def value_rows(s, r, token):
+    """[kv_heads][dim] of a token's values, to be written."""
+    return s["v"][int(s["table"][r, token // s["page"]]), :, token % s["page"]]
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_infinite_values_are_infinite_outputs(dim):
+    """One infinite value in a dim gives that infinity, both signs give NaN, other dims and heads are as before:
+    a request of one token, and tokens at every place of tiles, waves and pieces."""
+    print(f"attention infinite values dim={dim}", flush=True)
+    lens = [1, 50, 140, 700, 3000]
+    s = make(lens, 6, 2, dim, 16)
+    for r, n in enumerate(lens):
+        for i, token in enumerate({0, n // 3, n // 2, n - 1}):
+            value_rows(s, r, token)[0, 3 + i] = float("inf")
+            value_rows(s, r, token)[1, 40 + i] = -float("inf")
+        value_rows(s, r, 0)[1, 50] = float("inf")
+        value_rows(s, r, n - 1)[1, 50] = -float("inf")      # the first token's where there is one
+    ref = check_extended(s, dim ** -0.5)
+    assert ref.isinf().any(-1).all() and ref[1:, 3:].isnan().any(-1).all()
+    check_extended(s, dim ** -0.5, window=45)
+
+
+@pytest.mark.parametrize("far", [60, 256])
+def test_an_infinite_value_of_a_token_that_hardly_counts(far):
+    """Its probability e^-far times infinity is infinity, also where the probability itself is below fp32's
+    range: before and after the token that counts, in its tile, another one and another piece."""
+    print(f"attention infinite values, {far} below the maximum", flush=True)
+    lens = [40, 40, 900, 900, 5000, 5000]
+    s = make(lens, 2, 2, 64, 16)
+    s["q"].zero_()
+    s["q"].view(6, 2, 64)[:, :, 0] = 16.0
+    s["k"].nan_to_num_(0.0).zero_()
+    for r, (top, other) in enumerate([(30, 2), (2, 30), (800, 3), (3, 800), (4900, 100), (100, 4900)]):
+        s["k"][int(s["table"][r, top // 16]), :, top % 16, 0] = far / 16
+        value_rows(s, r, other)[:, 7] = float("inf")
+        value_rows(s, r, other)[0, 9] = -float("inf")
+    ref = check_extended(s, 1.0)
+    assert (ref[:, :, 7] == float("inf")).all() and (ref[:, 0, 9] == -float("inf")).all()
+
+
+def test_an_infinite_value_beside_one_that_is_not_a_number():
+    s = make([600, 33], 2, 2, 128, 16)
+    value_rows(s, 0, 17)[:, 5], value_rows(s, 0, 599)[:, 6] = float("inf"), float("nan")
+    value_rows(s, 1, 32)[:, 5], value_rows(s, 1, 0)[:, 5] = float("inf"), float("nan")
+    check_extended(s, 0.1)
