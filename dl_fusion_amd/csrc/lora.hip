@@ -440,11 +440,14 @@ __global__ __launch_bounds__(64 * kWaves, 2) void lora_out_kernel(const LoraArgs
         const uint32_t at = static_cast<uint32_t>(cb) * static_cast<uint32_t>(block_bytes) + 16 * (q ^ (q >> 4 & 15));
         load_lds16_buf(br, j < block_kb ? at : kOutOfRange, to + 1024 * j);
     };
+    // hi stops at bf16's largest value, so that a value just beyond it has its rest in lo, an infinity is lo's (a lo of
+    // inf - inf would be NaN), and NaN as well
     auto split = [](const f32x4_t& v, float scale, uint32_t* hi, uint32_t* lo) {
+        constexpr float kTop = 0x1.FEp127f;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const float x = v[2 * e] * scale, y = v[2 * e + 1] * scale;
-            hi[e] = pack_bf16x2(x, y);
+            hi[e] = pack_bf16x2(__builtin_amdgcn_fmed3f(x, -kTop, kTop), __builtin_amdgcn_fmed3f(y, -kTop, kTop));
             lo[e] = pack_bf16x2(x - __uint_as_float(hi[e] << 16), y - __uint_as_float(hi[e] & 0xFFFF0000u));
         }
     };
@@ -533,6 +536,35 @@ __global__ __launch_bounds__(64 * kWaves, 2) void lora_out_kernel(const LoraArgs
                 for (int i = 0; i < F; ++i)
                     y[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, bf[s][i]),
                                                                    __builtin_bit_cast(bf16x8_t, part ? lo[s] : hi[s]), y[i], 0, 0, 0);
+        // A weight of infinity has become NaN where lo is 0 or against hi.  So where there is a NaN, once more with the
+        // weights that are not finite apart: hi meets them alone, lo something finite of their sign.
+        f32x4_t all = y[0];
+#pragma unroll
+        for (int i = 1; i < F; ++i) all += y[i];
+        if (__builtin_expect(__ballot(__builtin_isnan(all[0] + all[1] + all[2] + all[3])) != 0, 0)) {
+#pragma unroll
+            for (int i = 0; i < F; ++i) {
+                y[i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int s = 0; s < RS; ++s) {
+                    u32x4_t finite, apart, sign;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t w = bf[s][i][e], bad = not_finite_bf16x2(w);
+                        finite[e] = w & ~bad;
+                        apart[e] = w & bad;
+                        sign[e] = finite[e] | (bad & (w & 0x80008000u | 0x3F803F80u));      // 1 or -1
+                    }
+                    auto add = [&](const u32x4_t& b16, const u32x4_t& h16) {
+                        y[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, b16),
+                                                                       __builtin_bit_cast(bf16x8_t, h16), y[i], 0, 0, 0);
+                    };
+                    add(finite, hi[s]);
+                    add(sign, lo[s]);
+                    add(apart, hi[s]);
+                }
+            }
+        }
         // lane: row li, columns 16 i + 4 g .. + 3
         wave_fence();
 #pragma unroll

@@ -541,7 +541,8 @@ dlf_status dlf_lora_workspace_bytes(const dlf_lora_desc *d, size_t *bytes);
  * and out[i] = base[i] where a is not in [0, adapters) or row_map[i] not in
  * [0, requests).  Rows may come in any order of their adapters.  The sums are
  * fp32, the inner vector x A^T enters the second product as a sum of two bf16
- * values, and out is rounded once.  As the residual of dlf_gemm_fused (base
+ * values, and out is rounded once.  Infinities and NaN go where the formula has
+ * them.  As the residual of dlf_gemm_fused (base
  * NULL, or the block's own residual) the sum with the projection is rounded
  * once more at most by the adapter's own share; base == out adds to a finished
  * projection in place.

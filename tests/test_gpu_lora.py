@@ -308,3 +308,51 @@ def test_a_weight_not_finite_stays_in_its_column(rank, bad):
         ref, tol = definition(s, s["ids"])
         rest = [c for c in range(136) if c not in cols]
         assert ((got.double() - ref).abs()[:, rest] <= tol[:, rest]).all()
+
+
+def check_extended(s):
+    """Infinities and NaN where the definition has them, the bound elsewhere."""
+    got = add(s).double()
+    ref, tol = definition(s, s["ids"])
+    assert torch.equal(got.isnan(), ref.isnan())
+    wide = ref.isinf()
+    assert torch.equal(got[wide], ref[wide])
+    rest = ref.isfinite()
+    assert ((got - ref).abs()[rest] <= tol[rest]).all()
+    return ref
+
+
+@pytest.mark.parametrize("rank", [8, 32, 40, 64, 80, 128])
+def test_infinities_stay_infinities(rank):
+    """An infinite input, an infinite weight of either product, and both: the formula's infinity, not NaN, but
+    where infinities of both signs meet or one meets zero."""
+    ids = few_and_many()
+    for what in ("x", "a", "b", "x and b"):
+        print(f"adapters rank={rank}, infinities in {what}", flush=True)
+        s = make(ids.numel(), 136, 264, rank, 3, ids, seed=16)
+        s["scale"] += 1
+        if "x" in what:
+            s["a"], s["b"] = s["a"].abs(), s["b"].abs()     # no two signs: the rows' outputs are infinities
+            s["x"][3, 7], s["x"][20, 263], s["x"][60, 0] = float("inf"), -float("inf"), float("inf")
+            s["b"][:, 9] = 0                                # but for this column
+        if "a" in what:
+            s["a"][1, rank - 1, 5] = float("inf")
+        if "b" in what:
+            s["b"][:, 40, 3], s["b"][:, 135, rank - 1] = float("inf"), -float("inf")
+            s["b"][:, 70, :2] = float("inf")                # NaN where the two ranks' signs differ
+        ref = check_extended(s)
+        assert ref.isinf().any() and ref.isfinite().any()
+
+
+@pytest.mark.parametrize("rank", [16, 64, 128])
+def test_an_inner_vector_at_the_end_of_the_range(rank):
+    """(2 - 2^-9) 2^127 is finite in fp32, and rounds to an infinity of bf16."""
+    ids = few_and_many()
+    s = make(ids.numel(), 136, 264, rank, 3, ids, scales=False, seed=17)
+    s["x"].zero_()
+    s["a"].zero_()
+    s["x"][:, 0], s["a"][:, :, 0] = (2 - 2.0 ** -7) * 2.0 ** 63, 2.0 ** 64
+    s["x"][:, 9], s["a"][:, :, 9] = 1.5 * 2.0 ** 60, 2.0 ** 59
+    s["b"] *= 2.0 ** -100
+    ref = check_extended(s)
+    assert ref.isfinite().all()
