@@ -164,6 +164,9 @@ struct FfnArgs {
 int ffn_parts(int64_t M, int D, int F);
 hipError_t launch_ffn(const FfnArgs& args, int act, hipStream_t stream);
 
+// A launch has fewer than 2^32 threads along x: workgroups of 256 have to stay below this.
+constexpr int64_t kMaxWorkgroups = int64_t(1) << 24;
+
 // Page plan: block tables and slot maps from request lengths (dlf_page_plan).
 struct PagePlanArgs {
     const int32_t* cached;      // [requests]
@@ -192,6 +195,7 @@ struct PagedStoreArgs {
     int kv_heads, head_dim, page_size;
     bool fp8;
 };
+int paged_store_tokens(int kv_heads, int head_dim);   // tokens that a workgroup takes
 hipError_t launch_paged_store(const PagedStoreArgs& args, hipStream_t stream);
 
 // Attention of one new token per request over the paged cache (dlf_paged_attention).

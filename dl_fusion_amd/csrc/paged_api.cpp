@@ -97,6 +97,10 @@ extern "C" dlf_status dlf_paged_store(const dlf_kv_cache_desc* c, int64_t tokens
         return fail(DLF_ERR_INVALID_ARG, "a row stride is below kv_heads * head_dim");
     if (k_stride % 8 != 0 || v_stride % 8 != 0 || k_stride > kMaxStride || v_stride > kMaxStride)
         return fail(DLF_ERR_UNSUPPORTED, "row strides must be multiples of 8, at most 2^31");
+    const int64_t each = dlf::paged_store_tokens(c->kv_heads, c->head_dim);
+    if ((tokens + each - 1) / each >= dlf::kMaxWorkgroups)
+        return fail(DLF_ERR_UNSUPPORTED, "tokens of %lld values must stay below %lld", static_cast<long long>(width),
+                    static_cast<long long>(each * (dlf::kMaxWorkgroups - 1) + 1));
     if (!k || !v || !slots || !k_cache || !v_cache)
         return fail(DLF_ERR_INVALID_ARG, "k, v, slots and the caches must be non-NULL");
     if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(slots, 8))
@@ -161,9 +165,8 @@ dlf_status check_attn_desc(const dlf_paged_attn_desc* d, dlf::PagedAttnArgs* a) 
     a->window = d->window;
     a->group = group;
     a->head_tiles = (group + 15) / 16;
-    if (static_cast<int64_t>(d->requests) * c->kv_heads * a->head_tiles >= (int64_t(1) << 31) ||
-        static_cast<int64_t>(d->requests) * d->heads >= (int64_t(1) << 31))
-        return fail(DLF_ERR_UNSUPPORTED, "requests * heads must stay below 2^31");
+    if (static_cast<int64_t>(d->requests) * c->kv_heads * a->head_tiles >= dlf::kMaxWorkgroups)
+        return fail(DLF_ERR_UNSUPPORTED, "requests * kv_heads * ceil(heads / kv_heads / 16) must stay below 2^24");
     const bool fp8 = c->dtype == DLF_FP8_E4M3;
     a->score_scale = static_cast<float>(static_cast<double>(d->softmax_scale) * (fp8 ? c->k_scale : 1.0f) *
                                         1.4426950408889634074);

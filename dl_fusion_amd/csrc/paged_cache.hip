@@ -300,10 +300,13 @@ hipError_t launch_page_plan(const PagePlanArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
+int paged_store_tokens(int kv_heads, int head_dim) {
+    const int chunks = kv_heads * (head_dim / 8);
+    return kStoreTogether * (chunks < kStoreThreads ? kStoreThreads / chunks : 1);
+}
+
 hipError_t launch_paged_store(const PagedStoreArgs& a, hipStream_t s) {
-    const int chunks = a.kv_heads * (a.head_dim / 8);
-    const int tokens = chunks < kStoreThreads ? kStoreThreads / chunks : 1;
-    const int each = tokens * kStoreTogether;
+    const int each = paged_store_tokens(a.kv_heads, a.head_dim);
     const dim3 grid(static_cast<unsigned>((a.tokens + each - 1) / each), 2);
     if (a.fp8) paged_store_kernel<true><<<grid, kStoreThreads, 0, s>>>(a);
     else paged_store_kernel<false><<<grid, kStoreThreads, 0, s>>>(a);

@@ -458,7 +458,10 @@ dlf_status dlf_page_plan(const dlf_page_plan_desc *d, const int32_t *cached, con
  *   slots     device [tokens] int64; a slot outside the cache (-1) is skipped.
  *             Two tokens with one slot: either is stored
  *   k_cache, v_cache  device, laid out as in dlf_kv_cache_desc
- * ALIAS: a cache overlaps an input or the other cache. */
+ * ALIAS: a cache overlaps an input or the other cache.  UNSUPPORTED: a row
+ * stride that is no multiple of 8 or above 2^31, more than 2^30 tokens, or more
+ * than 2^24 - 1 workgroups take, 4 max(1, floor(2048 / (kv_heads * head_dim)))
+ * tokens each. */
 dlf_status dlf_paged_store(const dlf_kv_cache_desc *c, int64_t tokens, const void *k, int64_t k_stride,
                            const void *v, int64_t v_stride, const int64_t *slots, void *k_cache,
                            void *v_cache, void *stream);
@@ -509,7 +512,9 @@ dlf_status dlf_paged_attention_workspace_bytes(const dlf_paged_attn_desc *d, siz
  *                operand; may be NULL where that size is 0.  Scratch: calls
  *                that share one on overlapping streams race
  * UNSUPPORTED: a head_dim, page_size or cache dtype not named above, more
- * than 256 query heads to a kv head, q_stride % 8 != 0. */
+ * than 256 query heads to a kv head, q_stride % 8 != 0 or above 2^31, more
+ * than 65536 requests, requests * kv_heads * ceil(heads / kv_heads / 16) of 2^24
+ * or more, max_pages * page_size >= 2^31. */
 dlf_status dlf_paged_attention(const dlf_paged_attn_desc *d, const void *q, const void *k_cache,
                                const void *v_cache, const int32_t *block_table, const int32_t *lens,
                                void *out, float *lse, void *workspace, size_t workspace_bytes,

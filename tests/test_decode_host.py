@@ -298,3 +298,26 @@ def test_adapters_binding_checks_shapes():
     for bx, by in ((x[:4], y), (wide, y), (x.t(), y), (x, y[:, :32]), (x, y.view(5, 8, 8))):
         with pytest.raises(ValueError):
             dlf.dlf_lora_add(d, bx, x, x, None, x, None, None, by, w, 4096, stream=0)
+
+
+# ---------------------------------------------------------------------------
+# Sizes that no launch can have: 2^24 workgroups of 256 threads
+# ---------------------------------------------------------------------------
+@fake_pointers
+def test_sizes_beyond_a_launch_are_refused():
+    wide = cache(kv_heads=256)
+    assert attn_bytes(attn(wide, heads=256, requests=65535)) == (dlf.DLF_OK, 0)
+    for d in (attn(wide, heads=256, requests=65536), attn(cache(kv_heads=128), heads=128 * 17, requests=65536),
+              attn(cache(kv_heads=1), heads=256, requests=65536, max_pages=1 << 20)):
+        refused = d.requests * d.cache.kv_heads * -(-d.heads // d.cache.kv_heads // 16) >= 1 << 24
+        assert attn_bytes(d) == ((UNSUPPORTED, 0) if refused else (dlf.DLF_OK, 0)), (d.heads, refused)
+        if refused:
+            assert call_attn(d) == UNSUPPORTED and "2^24" in dlf.dlf_last_error()
+    # 4 tokens a workgroup from 1032 values a token on, 128 at 64 values
+    for heads, dim, first in ((32, 256, (1 << 26) - 3), (17, 64, (1 << 26) - 3), (16, 64, (1 << 27) - 7),
+                              (4, 64, (1 << 29) - 31)):
+        c, w = cache(kv_heads=heads, head_dim=dim), heads * dim
+        assert call_store(c, tokens=first, ks=w, vs=w) == UNSUPPORTED, (heads, dim)
+        assert "values must stay below %d" % first in dlf.dlf_last_error()
+        # one less passes this check, and is refused for a pointer
+        assert call_store(c, tokens=first - 1, ks=w, vs=w, k=None) == INVALID, (heads, dim)
