@@ -369,12 +369,61 @@ def dlf_ffn_fused_noalloc(desc, x, w1_packed, b1, w2_packed, b2, residual, y, st
                                       _dev(b2), _dev(residual), _dev(y), _stream(stream)), "dlf_ffn_fused_noalloc")
 
 
-def _rows(t, rank):
-    """(device pointer, elements between rows) of a torch tensor whose dimensions after the first
+# What the operators of a decode step take for a type beside itself: its bits
+_I32, _I64, _F32, _BF16, _FP8 = torch.int32, torch.int64, torch.float32, torch.bfloat16, torch.float8_e4m3fn
+_BITS = {_BF16: (torch.int16, torch.uint16), _FP8: (torch.uint8, torch.int8)}
+
+
+def _refuse(t, dtype, size, name):
+    if t.dtype is not dtype and t.dtype not in _BITS.get(dtype, ()):
+        raise ValueError(f"{name} has type {t.dtype}, {dtype} is needed")
+    if t.nbytes < size:
+        raise ValueError(f"{name} has {t.nbytes} bytes, {size} are needed")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _sized(t, dtype, size, name):
+    """Device pointer of a contiguous torch tensor of ``dtype`` and at least ``size`` bytes, or a raw address
+    or None as it is: these operators read indices out of their arrays, so a short one or one of another type
+    would be read out of range.  Type and size take 0.05 to 0.1 us an array."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.dtype is not dtype or t.nbytes < size or not t.is_contiguous():
+        _refuse(t, dtype, size, name)
+    return t.data_ptr()
+
+
+def _table(t, rows, cols):
+    """The same of a block table, whose rows are as long as the descriptor says."""
+    size = 4 * rows * cols
+    if t is not None and not isinstance(t, int) and t.nbytes != size and t.dim() > 1 and t.shape[-1] != cols:
+        raise ValueError(f"block_table has {t.shape[-1]} columns, max_pages is {cols}")
+    return _sized(t, _I32, size, "block_table")
+
+
+def _workspace(t, size):
+    if t is None or isinstance(t, int):
+        return t
+    if t.nbytes < size or not t.is_contiguous():
+        raise ValueError(f"workspace must be contiguous, of at least {size} bytes")
+    return t.data_ptr()
+
+
+def _caches(cache, k_cache, v_cache):
+    dtype, size = (_FP8, 1) if cache.dtype == DLF_FP8_E4M3 else (_BF16, 2)
+    size *= cache.pages * cache.kv_heads * cache.page_size * cache.head_dim
+    return _sized(k_cache, dtype, size, "k_cache"), _sized(v_cache, dtype, size, "v_cache")
+
+
+def _rows(t, rank, name):
+    """(device pointer, elements between rows) of a bf16 torch tensor whose dimensions after the first
     are contiguous: [rows][...] with `rank` dimensions, 2 or 3; the first may have any stride."""
     shape, strides = t.shape, t.stride()
     if len(strides) != rank:
-        raise ValueError(f"a tensor of {rank} dimensions is needed, got {len(strides)}")
+        raise ValueError(f"{name} needs {rank} dimensions, got {len(strides)}")
+    if t.dtype is not _BF16 and t.dtype not in _BITS[_BF16]:
+        raise ValueError(f"{name} has type {t.dtype}, bf16 is needed")
     width = shape[-1]
     if strides[-1] != 1 and width != 1:
         raise ValueError("the dimensions after the first must be contiguous")
@@ -388,21 +437,26 @@ def _rows(t, rank):
 def dlf_page_plan(desc, cached, fresh, free_pages, free_head, block_table, starts, lens, slots, rows, counts,
                   stream=None):
     """Block tables and slot maps of a step, from the requests' lengths (see include/dlfusion.h)."""
-    _check(_lib.dlf_page_plan(ctypes.byref(desc), _dev(cached), _dev(fresh), _dev(free_pages), _dev(free_head),
-                              _dev(block_table), _dev(starts), _dev(lens), _dev(slots), _dev(rows), _dev(counts),
-                              _stream(stream)), "dlf_page_plan")
+    n, cap = desc.requests, desc.token_cap
+    _check(_lib.dlf_page_plan(ctypes.byref(desc), _sized(cached, _I32, 4 * n, "cached"),
+                              _sized(fresh, _I32, 4 * n, "fresh"),
+                              _sized(free_pages, _I32, 4 * desc.free_cap, "free_pages"),
+                              _sized(free_head, _I32, 4, "free_head"), _table(block_table, n, desc.max_pages),
+                              _sized(starts, _I32, 4 * n + 4, "starts"), _sized(lens, _I32, 4 * n, "lens"),
+                              _sized(slots, _I64, 8 * cap, "slots"), _sized(rows, _I32, 4 * cap, "rows"),
+                              _sized(counts, _I32, 16, "counts"), _stream(stream)), "dlf_page_plan")
 
 
 def dlf_paged_store(cache, k, v, slots, k_cache, v_cache, stream=None):
     """New keys and values [tokens][kv_heads][head_dim] into the cache's slots; the rows of k and v
     may be any distance apart (column blocks of a fused QKV product)."""
-    kp, ks = _rows(k, 3)
-    vp, vs = _rows(v, 3)
+    kp, ks = _rows(k, 3, "k")
+    vp, vs = _rows(v, 3, "v")
     tokens = k.shape[0]
-    if k.shape != v.shape or tuple(k.shape[1:]) != (cache.kv_heads, cache.head_dim) or slots.shape[0] != tokens:
+    if k.shape != v.shape or k.shape[1:] != (cache.kv_heads, cache.head_dim) or slots.shape[0] != tokens:
         raise ValueError("k and v must be [tokens][kv_heads][head_dim], slots [tokens]")
-    _check(_lib.dlf_paged_store(ctypes.byref(cache), tokens, kp, ks, vp, vs, _dev(slots), _dev(k_cache), _dev(v_cache),
-                                _stream(stream)), "dlf_paged_store")
+    _check(_lib.dlf_paged_store(ctypes.byref(cache), tokens, kp, ks, vp, vs, _sized(slots, _I64, 8 * tokens, "slots"),
+                                *_caches(cache, k_cache, v_cache), _stream(stream)), "dlf_paged_store")
 
 
 def dlf_paged_attention_workspace_bytes(desc):
@@ -416,16 +470,20 @@ def dlf_paged_attention(desc, q, k_cache, v_cache, block_table, lens, out, lse, 
                         stream=None):
     """Attention of one new token per request over the paged cache.  q is [requests][heads][head_dim]
     with its requests desc.q_stride elements apart (a column block of a fused QKV product)."""
+    n, heads, cache = desc.requests, desc.heads, desc.cache
+    dim = cache.head_dim
     if isinstance(q, int):
         qp = q
     else:
-        qp, qs = _rows(q, 3)
-        if tuple(q.shape) != (desc.requests, desc.heads, desc.cache.head_dim) or (q.shape[0] > 1 and
-                                                                                  qs != desc.q_stride):
+        qp, qs = _rows(q, 3, "q")
+        if q.shape != (n, heads, dim) or (n > 1 and qs != desc.q_stride):
             raise ValueError("q must be [requests][heads][head_dim], its requests q_stride elements apart")
-    _check(_lib.dlf_paged_attention(ctypes.byref(desc), qp, _dev(k_cache), _dev(v_cache), _dev(block_table),
-                                    _dev(lens), _dev(out), _dev(lse), _dev(workspace), int(workspace_bytes),
-                                    _stream(stream)), "dlf_paged_attention")
+    workspace_bytes = int(workspace_bytes)
+    _check(_lib.dlf_paged_attention(ctypes.byref(desc), qp, *_caches(cache, k_cache, v_cache),
+                                    _table(block_table, n, desc.max_pages), _sized(lens, _I32, 4 * n, "lens"),
+                                    _sized(out, _BF16, 2 * n * heads * dim, "out"),
+                                    _sized(lse, _F32, 4 * n * heads, "lse"), _workspace(workspace, workspace_bytes),
+                                    workspace_bytes, _stream(stream)), "dlf_paged_attention")
 
 
 def dlf_lora_workspace_bytes(desc):
@@ -435,11 +493,11 @@ def dlf_lora_workspace_bytes(desc):
 
 
 def _matrix(t, rows, cols, stride, name):
-    """Device pointer of a [rows][cols] tensor whose rows are `stride` elements apart, or of a raw
+    """Device pointer of a bf16 [rows][cols] tensor whose rows are `stride` elements apart, or of a raw
     address or None as it is."""
     if t is None or isinstance(t, int):
         return t
-    p, s = _rows(t, 2)
+    p, s = _rows(t, 2, name)
     if t.shape[0] != rows or t.shape[1] != cols or (rows > 1 and s != stride):
         raise ValueError(f"{name} must be [{rows}][{cols}] with rows {stride} elements apart")
     return p
@@ -448,11 +506,16 @@ def _matrix(t, rows, cols, stride, name):
 def dlf_lora_add(desc, x, a, b, scale, ids, row_map, base, out, workspace, workspace_bytes, stream=None):
     """out = base + scale (x A^T) B^T by each row's own adapter (see include/dlfusion.h); the rows of
     x, base and out lie the descriptor's strides apart."""
-    _check(_lib.dlf_lora_add(ctypes.byref(desc), _matrix(x, desc.m, desc.k, desc.x_stride, "x"), _dev(a), _dev(b),
-                             _dev(scale), _dev(ids), _dev(row_map),
-                             _matrix(base, desc.m, desc.n, desc.base_stride, "base"),
-                             _matrix(out, desc.m, desc.n, desc.out_stride, "out"), _dev(workspace),
-                             int(workspace_bytes), _stream(stream)), "dlf_lora_add")
+    m, n, k, count = desc.m, desc.n, desc.k, desc.adapters
+    weights = 2 * count * desc.rank
+    workspace_bytes = int(workspace_bytes)
+    _check(_lib.dlf_lora_add(ctypes.byref(desc), _matrix(x, m, k, desc.x_stride, "x"),
+                             _sized(a, _BF16, weights * k, "a"), _sized(b, _BF16, weights * n, "b"),
+                             _sized(scale, _F32, 4 * count, "scale"),
+                             _sized(ids, _I32, 4 * (m if row_map is None else desc.requests), "ids"),
+                             _sized(row_map, _I32, 4 * m, "row_map"), _matrix(base, m, n, desc.base_stride, "base"),
+                             _matrix(out, m, n, desc.out_stride, "out"), _workspace(workspace, workspace_bytes),
+                             workspace_bytes, _stream(stream)), "dlf_lora_add")
 
 
 def dlf_clock_probe(workgroups, iters, stamps, stream=None):

@@ -321,3 +321,75 @@ def test_sizes_beyond_a_launch_are_refused():
         assert "values must stay below %d" % first in dlf.dlf_last_error()
         # one less passes this check, and is refused for a pointer
         assert call_store(c, tokens=first - 1, ks=w, vs=w, k=None) == INVALID, (heads, dim)
+
+
+# ---------------------------------------------------------------------------
+# The binding compares its tensors with the descriptor
+# ---------------------------------------------------------------------------
+def _calls():
+    """entry point -> (call of a dict of tensors, the tensors); all as they should be."""
+    import torch
+    i32, i64, bf16, f32 = torch.int32, torch.int64, torch.bfloat16, torch.float32
+    z = lambda dtype, *shape: torch.zeros(*shape, dtype=dtype)  # noqa: E731
+    c, c8 = cache(), cache(dtype="fp8")
+    plan = dlf.page_plan_desc(8, 16, 4, 32, 64)
+    pool = (8, 2, 16, 64)
+    d = attn(max_pages=1 << 12)
+    size = dlf.dlf_paged_attention_workspace_bytes(d)
+    lo = lora()
+    lsize = dlf.dlf_lora_workspace_bytes(lo)
+    u8 = torch.uint8
+    return {
+        "plan": (lambda t: dlf.dlf_page_plan(plan, *t.values(), stream=0),
+                 dict(cached=z(i32, 8), fresh=z(i32, 8), free_pages=z(i32, 64), free_head=z(i32, 1),
+                      block_table=z(i32, 8, 4), starts=z(i32, 9), lens=z(i32, 8), slots=z(i64, 32), rows=z(i32, 32),
+                      counts=z(i32, 4))),
+        "store": (lambda t: dlf.dlf_paged_store(c, *t.values(), stream=0),
+                  dict(k=z(bf16, 4, 2, 64), v=z(bf16, 4, 2, 64), slots=z(i64, 4), k_cache=z(bf16, *pool),
+                       v_cache=z(bf16, *pool))),
+        "store fp8": (lambda t: dlf.dlf_paged_store(c8, *t.values(), stream=0),
+                      dict(k=z(bf16, 4, 2, 64), v=z(bf16, 4, 2, 64), slots=z(i64, 4),
+                           k_cache=z(torch.float8_e4m3fn, *pool), v_cache=z(u8, *pool))),
+        "attention": (lambda t: dlf.dlf_paged_attention(d, *t.values(), size, stream=0),
+                      dict(q=z(bf16, 4, 8, 64), k_cache=z(bf16, *pool), v_cache=z(bf16, *pool),
+                           block_table=z(i32, 4, 1 << 12), lens=z(i32, 4), out=z(bf16, 4, 8, 64), lse=z(f32, 4, 8),
+                           workspace=z(u8, size))),
+        "adapters": (lambda t: dlf.dlf_lora_add(lo, *t.values(), lsize, stream=0),
+                     dict(x=z(bf16, 5, 96), a=z(bf16, 3, 16, 96), b=z(bf16, 3, 64, 16), scale=z(f32, 3), ids=z(i32, 2),
+                          row_map=z(i32, 5), base=z(bf16, 5, 64), out=z(bf16, 5, 64), workspace=z(u8, lsize))),
+    }
+
+
+@fake_pointers
+@pytest.mark.parametrize("name", ["plan", "store", "store fp8", "attention", "adapters"])
+def test_binding_refuses_arrays_unlike_the_descriptor(name):
+    """Short ones, another type's and ones with gaps; every operand in turn."""
+    torch = pytest.importorskip("torch")
+    call, good = _calls()[name]
+    with pytest.raises(dlf.DlfError) as e:      # as they should be: it gets as far as the launch
+        call(good)
+    assert e.value.status == dlf.DLF_ERR_HIP
+    for n, t in good.items():
+        short = t.reshape(-1)[:-1]
+        gaps = torch.zeros(2 * t.numel(), dtype=t.dtype).view(*t.shape[:-1], -1)[..., ::2]
+        other = [] if n == "workspace" else [t.to({torch.int32: torch.int64, torch.int64: torch.int32}.get(t.dtype, torch.float16))]
+        if n == "free_head":                    # one number: nothing can lie between
+            gaps = short
+        for bad in (short, gaps, *other):
+            with pytest.raises(ValueError):
+                call({**good, n: bad})
+    if "block_table" in good:
+        t = good["block_table"]
+        for cols in (t.shape[1] - 1, t.shape[1] + 1):
+            with pytest.raises(ValueError, match="max_pages"):
+                call({**good, "block_table": torch.zeros(t.shape[0], cols, dtype=torch.int32)})
+
+
+@fake_pointers
+def test_binding_wants_an_id_for_every_row_or_request():
+    torch = pytest.importorskip("torch")
+    call, good = _calls()["adapters"]
+    with pytest.raises(ValueError, match="ids"):        # without a row map there are m of them, not `requests`
+        call({**good, "row_map": None})
+    with pytest.raises(dlf.DlfError):
+        call({**good, "row_map": None, "ids": torch.zeros(5, dtype=torch.int32)})
