@@ -54,23 +54,43 @@ class PagedAttentionBlock:
         bf16 = dict(dtype=torch.bfloat16, device=device)
         self.attended = torch.empty(requests, heads, head_dim, **bf16)
         self.attn_ws = torch.empty(dlf_paged_attention_workspace_bytes(self.attn), dtype=torch.uint8, device=device)
-        self._rows = {}         # buffers of a step of so many rows
+        self._step = self._prompts = None       # buffers, made when they are needed
 
     def _buffers(self, m):
-        got = self._rows.get(m)
-        if got is None:
-            device = self.w_qkv.device
-            got = dict(plan=page_plan_desc(self.requests, self.page_size, self.max_pages, m, self.free.numel()),
-                       slots=torch.empty(m, dtype=torch.int64, device=device),
-                       rows=torch.empty(m, dtype=torch.int32, device=device),
-                       qkv=torch.empty(m, self.width, dtype=torch.bfloat16, device=device),
-                       product=gemm_desc(m, self.width, self.hidden))
-            if self.adapters is not None:
-                count, rank, _ = self.adapters[0].shape
-                # the rows of a batch of prompts name their requests, those of a step are the requests
-                got["lora"] = lora_desc(m, self.width, self.hidden, rank, count, self.requests)
-                got["lora_ws"] = torch.empty(dlf_lora_workspace_bytes(got["lora"]), dtype=torch.uint8, device=device)
-            self._rows[m] = got
+        """What m rows need.  A step's buffers are its own and stay where they are, as a captured graph needs
+        them; batches of prompts of any length share one set, which grows to the longest."""
+        if m == self.requests:
+            if self._step is None:
+                self._step = self._views(m, self._allocate(m))
+            return self._step
+        if self._prompts is None or self._prompts["rows"].numel() < m or (
+                self.adapters is not None and self._prompts["lora_ws"].numel() < self._lora(m)[1]):
+            most, ws = (0, 0) if self._prompts is None else (self._prompts[n].numel() for n in ("rows", "lora_ws"))
+            self._prompts = None            # before the next is made
+            self._prompts = self._allocate(max(m, most), ws)
+        return self._views(m, self._prompts)
+
+    def _lora(self, m):
+        count, rank, _ = self.adapters[0].shape
+        # the rows of a batch of prompts name their requests, those of a step are the requests
+        d = lora_desc(m, self.width, self.hidden, rank, count, self.requests)
+        return d, dlf_lora_workspace_bytes(d)
+
+    def _allocate(self, m, lora_ws=0):
+        device = self.w_qkv.device
+        if self.adapters is not None:
+            lora_ws = max(lora_ws, self._lora(m)[1])
+        return dict(slots=torch.empty(m, dtype=torch.int64, device=device),
+                    rows=torch.empty(m, dtype=torch.int32, device=device),
+                    qkv=torch.empty(m, self.width, dtype=torch.bfloat16, device=device),
+                    lora_ws=torch.empty(lora_ws, dtype=torch.uint8, device=device))
+
+    def _views(self, m, room):
+        got = dict(plan=page_plan_desc(self.requests, self.page_size, self.max_pages, m, self.free.numel()),
+                   product=gemm_desc(m, self.width, self.hidden), lora_ws=room["lora_ws"],
+                   **{n: room[n][:m] for n in ("slots", "rows", "qkv")})
+        if self.adapters is not None:
+            got["lora"] = self._lora(m)[0]
         return got
 
     def _project(self, x, b, row_map):
@@ -94,7 +114,8 @@ class PagedAttentionBlock:
 
     def admit(self, x, fresh):
         """Keys and values of prompts into the cache: ``fresh`` [requests] int32, how many tokens each place
-        brings, and their rows x [tokens][hidden], request by request (more rows than tokens are padding)."""
+        brings, and their rows x [tokens][hidden], request by request (more rows than tokens are padding).  Not to be
+        captured: a longer batch of prompts moves the buffers."""
         b = self._buffers(x.shape[0])
         self._plan(b, fresh)
         self._project(x, b, b["rows"])

@@ -393,3 +393,42 @@ def test_binding_wants_an_id_for_every_row_or_request():
         call({**good, "row_map": None})
     with pytest.raises(dlf.DlfError):
         call({**good, "row_map": None, "ids": torch.zeros(5, dtype=torch.int32)})
+
+
+# ---------------------------------------------------------------------------
+# The attention block (dl_fusion_amd/decode.py): its buffers, made on the CPU
+# ---------------------------------------------------------------------------
+def block_on_the_cpu(adapters=True, requests=4, pages=64):
+    torch = pytest.importorskip("torch")
+    from dl_fusion_amd.decode import PagedAttentionBlock
+    w = lambda *shape: torch.zeros(*shape, dtype=torch.bfloat16)  # noqa: E731
+    ad = (w(3, 16, 128), w(3, 512, 16), None) if adapters else None
+    return PagedAttentionBlock(w(512, 128), w(128, 256), 4, 2, 64, requests, pages, 16, 16, ad)
+
+
+def tensor_bytes():
+    import gc
+    import torch
+    gc.collect()
+    stores = [o.untyped_storage() for o in gc.get_objects() if issubclass(type(o), torch.Tensor)]
+    return sum({s.data_ptr(): s.nbytes() for s in stores}.values())
+
+
+@pytest.mark.parametrize("adapters", [False, True])
+def test_prompts_of_any_length_share_their_buffers(adapters):
+    block = block_on_the_cpu(adapters)
+    step = block._buffers(4)
+    start = tensor_bytes()
+    block._buffers(3000)
+    longest = tensor_bytes() - start
+    assert longest >= 3000 * 512 * 2
+    for m in [*range(5, 700, 13), 2999, 3000, 1]:
+        b = block._buffers(m)
+        assert [b[n].shape[0] for n in ("slots", "rows", "qkv")] == [m, m, m] and b["qkv"].is_contiguous()
+        if adapters:
+            assert b["lora"].m == m and b["lora_ws"].numel() >= dlf.dlf_lora_workspace_bytes(b["lora"])
+        assert b["plan"].token_cap == m
+        del b
+    assert tensor_bytes() - start <= longest * 1.5          # a short batch's workspace may be the larger one
+    again = block._buffers(4)
+    assert all(again[n].data_ptr() == step[n].data_ptr() for n in ("slots", "rows", "qkv", "lora_ws") if n in step)

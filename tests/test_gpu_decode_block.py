@@ -161,3 +161,51 @@ def test_a_captured_step_follows_the_requests():
         for name in ("table", "lens", "cached", "head", "attended"):
             assert torch.equal(getattr(a, name), getattr(b, name)), (i, name)
         assert torch.equal(ya, yb), i
+
+
+def captured(step):
+    """`step` run once and captured."""
+    step()
+    torch.cuda.synchronize()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        with torch.cuda.graph(graph, stream=side):
+            step()
+    torch.cuda.current_stream().wait_stream(side)
+    return graph
+
+
+def same_block(a, requests, g):
+    b = build(requests, g)
+    for name in ("w_qkv", "w_o", "adapters"):
+        setattr(b, name, getattr(a, name))
+    return b
+
+
+def test_prompts_of_growing_length_between_replays():
+    """The prompts' buffers move as they grow, the captured step's do not."""
+    g = torch.Generator().manual_seed(21)
+    requests = 3
+    a = build(requests, g)
+    b = same_block(a, requests, g)
+    for block in (a, b):
+        block.ids.copy_(torch.tensor([0, -1, 2]))
+    xs, one = rand(g, requests, HIDDEN), torch.ones(requests, dtype=torch.int32, device="cuda")
+    ya, yb = (torch.empty(requests, HIDDEN, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    b.step(xs, one, yb)
+    graph = captured(lambda: a.step(xs, one, ya))       # counts as one step: capturing runs nothing
+    for lengths in ([5, 0, 1], [40, 33, 0], [1, 2, 4], [200, 100, 300]):
+        print(f"decode block prompts {lengths} between replays", flush=True)
+        x = rand(g, sum(lengths), HIDDEN)
+        xs.copy_(rand(g, requests, HIDDEN))
+        fresh = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+        for block in (a, b):
+            block.admit(x, fresh)
+        graph.replay()
+        torch.cuda.synchronize()
+        b.step(xs, one, yb)
+        torch.cuda.synchronize()
+        for name in ("table", "lens", "cached", "head", "attended"):
+            assert torch.equal(getattr(a, name), getattr(b, name)), name
+        assert torch.equal(ya, yb)
