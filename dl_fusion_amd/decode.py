@@ -11,7 +11,9 @@ pages of one pool.  A step enqueues, on the current stream and without reading a
     dlf_gemm_fused       the output projection with the residual
 
 so that it can be captured in a graph and replayed while requests grow, join and leave: their lengths,
-tokens, pages and adapters are read from device memory.  ``python -m dl_fusion_amd.decode`` runs a batch.
+tokens, pages and adapters are read from device memory.  ``admit`` brings a request's prompt to a place,
+``release`` gives a place's pages back.  Where the pool has no page left, a token is not stored, its
+request stays as long as it was, and ``short`` says so.  ``python -m dl_fusion_amd.decode`` runs a batch.
 """
 from __future__ import annotations
 
@@ -40,12 +42,17 @@ class PagedAttentionBlock:
         shape = (pages, kv_heads, page_size, head_dim)
         dtype = torch.float8_e4m3fn if cache == "fp8" else torch.bfloat16
         self.k_cache, self.v_cache = (torch.zeros(shape, dtype=dtype, device=device) for _ in range(2))
-        # the requests' state: tokens cached, pages held, adapters; and the pool's free pages from `head` on
+        # the requests' state: tokens stored, the pages that hold them, adapters; and the pool's free pages from `head`
+        # on (one entry more, for release() to write to)
         self.cached = torch.zeros(requests, **i32)
         self.table = torch.full((requests, max_pages), -1, **i32)
         self.ids = torch.full((requests,), -1, **i32)
-        self.free = torch.arange(pages, **i32)
+        self._free = torch.arange(pages + 1, **i32)
+        self.free = self._free[:pages]
         self.head = torch.zeros(1, **i32)
+        # fresh tokens of the last admit or step, and those of them that were stored; a step's slots, and one for nobody
+        self._asked, self._stored = torch.zeros(requests, **i32), torch.zeros(requests, **i32)
+        self._slots = torch.empty(requests + 1, dtype=torch.int64, device=device)
         # what a step plans
         self.starts, self.lens = torch.empty(requests + 1, **i32), torch.empty(requests, **i32)
         self.counts = torch.empty(4, **i32)
@@ -108,33 +115,66 @@ class PagedAttentionBlock:
     def _plan(self, b, fresh):
         dlf_page_plan(b["plan"], self.cached, fresh, self.free, self.head, self.table, self.starts, self.lens,
                       b["slots"], b["rows"], self.counts)
-        # the next step's state, in the order of the stream: what follows reads lens
-        self.cached.copy_(self.lens)
         self.head.copy_(self.counts[1:2])
+
+    @property
+    def short(self):
+        """[requests] int32: the fresh tokens of the last admit or step that were not stored."""
+        return self._asked - self._stored
 
     def admit(self, x, fresh):
         """Keys and values of prompts into the cache: ``fresh`` [requests] int32, how many tokens each place
-        brings, and their rows x [tokens][hidden], request by request (more rows than tokens are padding).  Not to be
-        captured: a longer batch of prompts moves the buffers."""
+        brings, and their rows x [tokens][hidden], request by request (more rows than tokens are padding).  Tokens
+        without a row, past the pool's last page or past the place's table are not stored, and counted in ``short``:
+        they are the last ones of their place, and may be brought again later.  Not to be captured: a longer batch of
+        prompts moves the buffers."""
         b = self._buffers(x.shape[0])
-        self._plan(b, fresh)
+        fresh = fresh.clamp(min=0)
+        # pages for the tokens that have a row only, or they would be nobody's
+        before = fresh.cumsum(0) - fresh
+        self._plan(b, torch.minimum(fresh, (x.shape[0] - before).clamp(min=0)).to(torch.int32))
         self._project(x, b, b["rows"])
         self._store(b, b["slots"])
+        # lengths grow by the tokens that have a slot: missing pages are asked for again by the next plan
+        self._asked.copy_(fresh)
+        self._stored.zero_().index_add_(0, b["rows"].clamp(min=0), (b["slots"] >= 0).to(torch.int32))
+        self.cached.add_(self._stored)
 
     def step(self, x, fresh, y):
         """One token for every place whose ``fresh`` (int32, 0 or 1) is 1: its row of x [requests][hidden] gives
-        its row of y.  Other places attend to what they have cached and store nothing."""
+        its row of y.  Other places attend to what they have cached and store nothing; so does a place whose token
+        finds no page, or whose table is full: its ``short`` is 1, its row of y not to be used, and the token may be
+        brought again once there are pages."""
         b = self._buffers(self.requests)
-        self._plan(b, fresh)
+        self._plan(b, torch.gt(fresh, 0, out=self._asked))
         self._project(x, b, None)
-        # the plan numbers the tokens; row r of x is place r
-        slots = b["slots"][self.starts[:-1].long().clamp(max=self.requests - 1)].masked_fill(fresh == 0, -1)
-        self._store(b, slots)
+        # the plan numbers the tokens, row r of x is place r; rows that no token has are -1, the last entry
+        self._slots.fill_(-1)[b["rows"]] = b["slots"]
+        self._store(b, self._slots[:-1])
+        self.cached.add_(torch.ge(self._slots[:-1], 0, out=self._stored))
         q = b["qkv"][:, :self.heads * self.head_dim].unflatten(1, (self.heads, self.head_dim))
-        dlf_paged_attention(self.attn, q, self.k_cache, self.v_cache, self.table, self.lens, self.attended, None,
+        dlf_paged_attention(self.attn, q, self.k_cache, self.v_cache, self.table, self.cached, self.attended, None,
                             self.attn_ws, self.attn_ws.numel())
         dlf_gemm_fused(gemm_desc(self.requests, self.hidden, self.heads * self.head_dim),
                        self.attended.view(self.requests, -1), self.w_o, None, None, x, y)
+
+    def release(self, leaving):
+        """Gives the pages of the places ``leaving`` (bool [requests], or their numbers) back to the pool and
+        empties the places.  Enqueued like a step, between steps or replays."""
+        if not isinstance(leaving, torch.Tensor):
+            gone = set(leaving)
+            leaving = torch.tensor([r in gone for r in range(self.requests)], device=self.cached.device)
+        cols = torch.arange(self.max_pages, device=self.cached.device)
+        held = leaving[:, None] & (cols < -(-self.cached // self.page_size)[:, None])
+        back = held.flatten().cumsum(0)
+        # the list's entries before `head` are taken pages', so that those that come back fit there
+        to = torch.where(held.flatten(), self.head - back[-1:] + back - 1, self.free.numel())
+        self._free.scatter_(0, to, self.table.flatten())
+        self.head.sub_(back[-1:])
+        self.table.masked_fill_(leaving[:, None], -1)
+        self.cached.masked_fill_(leaving, 0)
+        self._asked.masked_fill_(leaving, 0)
+        self._stored.masked_fill_(leaving, 0)
 
 
 def main():

@@ -432,3 +432,144 @@ def test_prompts_of_any_length_share_their_buffers(adapters):
     assert tensor_bytes() - start <= longest * 1.5          # a short batch's workspace may be the larger one
     again = block._buffers(4)
     assert all(again[n].data_ptr() == step[n].data_ptr() for n in ("slots", "rows", "qkv", "lora_ws") if n in step)
+
+
+# ---------------------------------------------------------------------------
+# The block's bookkeeping, its kernels replaced by Python on the CPU: places join, grow, leave and run out of
+# pages, and every place holds just the tokens that a plain list of them says
+# ---------------------------------------------------------------------------
+PAGE, COLS = 16, 4
+
+
+def up(n):
+    return -(-n // PAGE)
+
+
+@pytest.fixture
+def kernels_in_python(monkeypatch):
+    from dl_fusion_amd import decode
+    cells, attended = {}, {}
+
+    def plan(desc, cached, fresh, free, head, table, starts, lens, slots, rows, counts):
+        cap, want, at = desc.max_pages * PAGE, int(head), 0
+        slots.fill_(-1)
+        rows.fill_(-1)
+        for r in range(desc.requests):
+            c, f = int(cached[r]), max(int(fresh[r]), 0)
+            starts[r], lens[r] = at, min(c + f, cap)
+            for col in range(up(min(c, cap)), up(int(lens[r]))):
+                table[r, col] = free[want] if want < desc.free_cap else -1
+                want += 1
+            for pos in range(c, c + f):
+                page = int(table[r, pos // PAGE]) if pos < cap else -1
+                if at < desc.token_cap:
+                    slots[at], rows[at] = (page * PAGE + pos % PAGE if page >= 0 else -1), r
+                at += 1
+        starts[desc.requests] = at
+        counts[0], counts[1], counts[2] = at, min(want, desc.free_cap), int(lens.max())
+        counts[3] = max(0, want - desc.free_cap)
+
+    def product(desc, a, b, scale, shift, residual, c):
+        c.copy_(a[:, :1].expand_as(c))          # a row's token number in all its columns
+
+    def store(cache, k, v, slots, k_cache, v_cache):
+        taken = [s for s in slots.tolist() if s >= 0]
+        assert len(set(taken)) == len(taken) and k.shape[0] == len(slots)
+        cells.update({s: int(k[i, 0, 0]) for i, s in enumerate(slots.tolist()) if s >= 0})
+
+    def attention(desc, q, k_cache, v_cache, table, lens, out, lse, ws, size):
+        attended["lens"], attended["table"] = lens.tolist(), table.tolist()
+        out.zero_()
+
+    for name, fn in (("dlf_page_plan", plan), ("dlf_gemm_fused", product), ("dlf_paged_store", store),
+                     ("dlf_paged_attention", attention)):
+        monkeypatch.setattr(decode, name, fn)
+    return cells, attended
+
+
+class Places:
+    """What the block should hold: a list of token numbers a place, and the number of pages."""
+
+    def __init__(self, requests, pages):
+        self.tokens, self.pages = [[] for _ in range(requests)], pages
+
+    def bring(self, news, rows):
+        """news: [place] -> token numbers; returns how many are not stored."""
+        free, short = self.pages - sum(up(len(t)) for t in self.tokens), []
+        for t, new in zip(self.tokens, news):
+            given = new[:rows]
+            rows -= len(given)
+            most = up(len(t)) + min(max(0, free), COLS - up(len(t)))
+            fits = given[:max(0, PAGE * most - len(t))]
+            free -= up(len(t) + len(fits)) - up(len(t))
+            t += fits
+            short.append(len(new) - len(fits))
+        return short
+
+
+def check_places(block, places, cells):
+    assert block.cached.tolist() == [len(t) for t in places.tokens]
+    pages = []
+    for r, t in enumerate(places.tokens):
+        mine = block.table[r, :up(len(t))].tolist()
+        assert [cells[mine[i // PAGE] * PAGE + i % PAGE] for i in range(len(t))] == t, r
+        pages += mine
+    assert int(block.head) == len(pages)
+    assert sorted(pages + block.free[len(pages):].tolist()) == list(range(places.pages))
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_places_join_grow_leave_and_run_out(kernels_in_python, seed):
+    import random
+    torch = pytest.importorskip("torch")
+    cells, attended = kernels_in_python
+    rng = random.Random(seed)
+    requests, pages = 5, [1, 9, 11, 13, 20, 0][seed] or 7
+    from dl_fusion_amd.decode import PagedAttentionBlock
+    w = lambda *shape: torch.zeros(*shape, dtype=torch.bfloat16)  # noqa: E731
+    block = PagedAttentionBlock(w(512, 128), w(128, 256), 4, 2, 64, requests, pages, PAGE, COLS)
+    places, number = Places(requests, pages), 0
+    y = w(requests, 128)
+
+    def numbers(count):
+        nonlocal number
+        number += count
+        return [(number - count + i) % 251 for i in range(count)]       # bf16 has integers to 256
+
+    def rows(tokens):
+        x = w(len(tokens), 128)
+        x[:, 0] = torch.tensor(tokens, dtype=torch.float32)
+        return x
+
+    ran_out = left = 0
+    for _ in range(120):
+        what = rng.choice(["admit", "step", "step", "step", "release"])
+        if what == "admit":
+            lengths = [rng.choice([0, 0, 1, rng.randrange(80)]) for _ in range(requests)]
+            news = [numbers(n) for n in lengths]
+            flat = [t for n in news for t in n]
+            m = max(1, len(flat) + rng.choice([0, 0, 3, -2, -30]))
+            if m == requests:
+                continue
+            short = places.bring(news, m)
+            block.admit(rows((flat + [250] * 3)[:m]), torch.tensor(lengths, dtype=torch.int32))
+        elif what == "step":
+            fresh = [rng.choice([0, 1, 1, 1, -3, 2]) for _ in range(requests)]
+            tokens = numbers(requests)
+            short = places.bring([[t] if f > 0 else [] for t, f in zip(tokens, fresh)], requests)
+            block.step(rows(tokens), torch.tensor(fresh, dtype=torch.int32), y)
+            assert attended["lens"] == [len(t) for t in places.tokens]
+            for r, t in enumerate(places.tokens):
+                assert min(attended["table"][r][:up(len(t))], default=0) >= 0
+        else:
+            leaving = [r for r in range(requests) if rng.random() < 0.3]
+            for r in leaving:
+                left += len(places.tokens[r])
+                places.tokens[r] = []
+            flags = torch.tensor([r in leaving for r in range(requests)])
+            block.release(leaving if rng.random() < 0.5 else flags)
+            short = [0 if r in leaving else n for r, n in enumerate(short)] if _ else [0] * requests
+        check_places(block, places, cells)
+        assert block.short.tolist() == short, what
+        ran_out += sum(short) > 0
+    assert ran_out and left

@@ -209,3 +209,60 @@ def test_prompts_of_growing_length_between_replays():
         for name in ("table", "lens", "cached", "head", "attended"):
             assert torch.equal(getattr(a, name), getattr(b, name)), name
         assert torch.equal(ya, yb)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "fp8"])
+def test_places_leave_and_run_out_of_pages_between_replays(cache):
+    """A captured step over a pool of 12 pages against eager steps over one that never ends: places that find no
+    page wait, places that leave give theirs back, and what is attended to is the same bits throughout."""
+    from dl_fusion_amd.decode import PagedAttentionBlock
+    g = torch.Generator().manual_seed(33)
+    requests = 3
+    b = build(requests, g, cache)
+    a = PagedAttentionBlock(b.w_qkv, b.w_o, HEADS, KV, DIM, requests, 12, PAGE, COLS, b.adapters, cache=cache,
+                            k_scale=0.0625, v_scale=0.0625)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    for block in (a, b):
+        block.ids.copy_(torch.tensor([0, -1, 2]))
+    xs, fresh = rand(g, requests, HIDDEN), torch.zeros(requests, **i32)
+    ya, yb = (torch.empty(requests, HIDDEN, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    graph = captured(lambda: a.step(xs, fresh, ya))
+    waited = 0
+
+    def admit(lengths):
+        x, n = rand(g, sum(lengths), HIDDEN), torch.tensor(lengths, **i32)
+        for block in (a, b):
+            block.admit(x, n)
+        assert not a.short.any() and not b.short.any()
+
+    def steps(count):
+        nonlocal waited
+        for _ in range(count):
+            xs.copy_(rand(g, requests, HIDDEN))
+            fresh.fill_(1)
+            graph.replay()
+            torch.cuda.synchronize()
+            waited += int(a.short.sum())
+            b.step(xs, fresh - a.short, yb)
+            torch.cuda.synchronize()
+            assert torch.equal(a.cached, b.cached) and not b.short.any()
+            assert torch.equal(a.attended, b.attended) and torch.equal(ya, yb)
+            held = [p for r in range(requests) for p in a.table[r, :-(-int(a.cached[r]) // PAGE)].tolist()]
+            assert sorted(held + a.free[int(a.head):].tolist()) == list(range(12))
+
+    print(f"decode block, 12 pages, {cache}", flush=True)
+    admit([40, 16, 100])
+    steps(10)                           # 3 + 1 + 7 pages, and then one more for place 1 and none for place 0
+    assert waited and a.cached.tolist()[0] == 48
+    for block in (a, b):
+        block.release([2])
+    steps(3)
+    admit([0, 0, 33])
+    steps(20)
+    for block in (a, b):
+        block.release(torch.tensor([True, True, False], device="cuda"))
+    admit([70, 1, 0])
+    steps(4)
+    for block in (a, b):
+        block.release(range(requests))
+    assert int(a.head) == 0 and (a.table == -1).all() and not a.cached.any()
