@@ -24,6 +24,12 @@ from . import (dlf_gemm_fused, dlf_lora_add, dlf_lora_workspace_bytes, dlf_page_
                page_plan_desc, paged_attn_desc)
 
 
+def _shaped(t, shape, name, dtype=torch.bfloat16):
+    """The products read as many values as their descriptors say, whatever the tensor holds."""
+    if tuple(t.shape) != shape or t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+
+
 class PagedAttentionBlock:
     """``w_qkv`` [(heads + 2 kv_heads) * head_dim][hidden] (queries, keys, values) and ``w_o``
     [hidden][heads * head_dim], bf16 on the device.  ``adapters``: (a [count][rank][hidden],
@@ -36,6 +42,15 @@ class PagedAttentionBlock:
         self.heads, self.kv_heads, self.head_dim, self.requests = heads, kv_heads, head_dim, requests
         self.page_size, self.max_pages = page_size, max_pages
         self.width, self.hidden = w_qkv.shape
+        _shaped(w_qkv, ((heads + 2 * kv_heads) * head_dim, self.hidden), "w_qkv")
+        _shaped(w_o, (self.hidden, heads * head_dim), "w_o")
+        if adapters is not None:
+            a, b, scale = adapters
+            count, rank, _ = a.shape
+            _shaped(a, (count, rank, self.hidden), "the adapters' a")
+            _shaped(b, (count, self.width, rank), "the adapters' b")
+            if scale is not None:
+                _shaped(scale, (count,), "the adapters' scale", torch.float32)
         device = w_qkv.device
         i32 = dict(dtype=torch.int32, device=device)
         self.cache = kv_cache_desc(pages, kv_heads, page_size, head_dim, cache, k_scale, v_scale)
@@ -128,6 +143,8 @@ class PagedAttentionBlock:
         without a row, past the pool's last page or past the place's table are not stored, and counted in ``short``:
         they are the last ones of their place, and may be brought again later.  Not to be captured: a longer batch of
         prompts moves the buffers."""
+        _shaped(x, (x.shape[0], self.hidden), "x")
+        _shaped(fresh, (self.requests,), "fresh", torch.int32)
         b = self._buffers(x.shape[0])
         fresh = fresh.clamp(min=0)
         # pages for the tokens that have a row only, or they would be nobody's
@@ -145,6 +162,9 @@ class PagedAttentionBlock:
         its row of y.  Other places attend to what they have cached and store nothing; so does a place whose token
         finds no page, or whose table is full: its ``short`` is 1, its row of y not to be used, and the token may be
         brought again once there are pages."""
+        for t, name in ((x, "x"), (y, "y")):
+            _shaped(t, (self.requests, self.hidden), name)
+        _shaped(fresh, (self.requests,), "fresh", torch.int32)
         b = self._buffers(self.requests)
         self._plan(b, torch.gt(fresh, 0, out=self._asked))
         self._project(x, b, None)

@@ -573,3 +573,27 @@ def test_places_join_grow_leave_and_run_out(kernels_in_python, seed):
         assert block.short.tolist() == short, what
         ran_out += sum(short) > 0
     assert ran_out and left
+
+
+def test_block_refuses_tensors_of_other_shapes(kernels_in_python):
+    torch = pytest.importorskip("torch")
+    from dl_fusion_amd.decode import PagedAttentionBlock
+    w = lambda *shape, dtype=torch.bfloat16: torch.zeros(*shape, dtype=dtype)  # noqa: E731
+    args = lambda **kw: {**dict(w_qkv=w(512, 128), w_o=w(128, 256), heads=4, kv_heads=2, head_dim=64, requests=3,  # noqa: E731
+                                pages=9, page_size=PAGE, max_pages=COLS), **kw}
+    PagedAttentionBlock(**args())
+    for bad in (dict(w_qkv=w(448, 128)), dict(w_o=w(128, 512)), dict(w_o=w(64, 256)), dict(w_qkv=w(512, 128, dtype=torch.float32)),
+                dict(adapters=(w(3, 16, 64), w(3, 512, 16), None)), dict(adapters=(w(3, 16, 128), w(2, 512, 16), None)),
+                dict(adapters=(w(3, 16, 128), w(3, 512, 8), None)), dict(adapters=(w(3, 16, 128), w(3, 512, 16), w(3)))):
+        with pytest.raises(ValueError):
+            PagedAttentionBlock(**args(**bad))
+    block = PagedAttentionBlock(**args())
+    x, y, one = w(3, 128), w(3, 128), torch.ones(3, dtype=torch.int32)
+    for call in (lambda: block.step(x[:2], one, y), lambda: block.step(x, one, y[:, :64]), lambda: block.step(x, one[:2], y),
+                 lambda: block.step(x, one.long(), y), lambda: block.step(x, one, y.float()),
+                 lambda: block.admit(w(7, 64), one), lambda: block.admit(w(7, 128), one[:2]),
+                 lambda: block.admit(w(7, 128), one.bool())):
+        with pytest.raises(ValueError):
+            call()
+    block.step(x, one, y)
+    block.admit(w(7, 128), one)
