@@ -456,7 +456,8 @@ dlf_status dlf_page_plan(const dlf_page_plan_desc *d, const int32_t *cached, con
  *             elements apart (a multiple of 8; >= kv_heads * head_dim): column
  *             blocks of a fused QKV product need no copy
  *   slots     device [tokens] int64; a slot outside the cache (-1) is skipped.
- *             Two tokens with one slot: either is stored
+ *             Two tokens with one slot leave a mixture of both there, of their keys
+ *             and values and of parts of a row
  *   k_cache, v_cache  device, laid out as in dlf_kv_cache_desc
  * ALIAS: a cache overlaps an input or the other cache.  UNSUPPORTED: a row
  * stride that is no multiple of 8 or above 2^31, more than 2^30 tokens, or more
