@@ -41,20 +41,6 @@ __device__ __forceinline__ int adapter_of(const LoraArgs& p, int row) {
 // this slot's; `there`: the lanes that have a row.
 template <class Fn>
 __device__ __forceinline__ void for_each_adapter(int id, uint64_t there, int slot, int slots, Fn&& f) {
-    if (slots > 8) {
-        // many turns: the first rows of all adapters at once, 63 comparisons, and of those every slots-th
-        uint64_t again = 0;
-#pragma unroll
-        for (int j = 0; j < 63; ++j) again |= __ballot(id == __builtin_amdgcn_readlane(id, j)) & (~uint64_t(0) << (j + 1));
-        uint64_t firsts = there & ~again;       // the rows are the first lanes
-        for (int turn = 0; firsts; ++turn, firsts &= firsts - 1) {
-            if (turn < slot) continue;
-            const int cur = __builtin_amdgcn_readlane(id, __builtin_ctzll(firsts));
-            f(cur, __ballot(id == cur) & there);
-            slot += slots;
-        }
-        return;
-    }
     int turn = 0;
     while (there) {
         const int cur = __builtin_amdgcn_readlane(id, __builtin_ctzll(there));
