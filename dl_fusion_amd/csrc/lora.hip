@@ -384,11 +384,18 @@ struct OutLds {
     static constexpr int kCols = kSteps == 4 ? 32 : 64;     // of a block
     static constexpr int kB = kCols * (SELF ? 16 * RF : 32 * kSteps) * 2;   // bytes of a block of B
     static constexpr int kBase = kTileRows * kCols * 2;     // and of base
+    // Blocks in the ring, for two workgroups a CU: five at ranks 33..64 are 96 KB, and 8192 rows at rank 64 take 75 us
+    // instead of 61 (three: 60; at ranks 65..128 three, four and five are 90, 91 and 91)
     static constexpr int kDepth = kSteps == 2 ? 4 : 5;
     static constexpr int kOwn = 16 * kCols * 4;             // a wave's 16 rows of products, fp32
-    static constexpr int kOwnBlocks = kSteps == 1 && !SELF ? 4 : 2;  // blocks that a wave has of its own at a time
+    // Blocks that a wave has of its own at a time.  As many as leave two workgroups a CU: four at ranks 33..64 take
+    // 64 rows of 64 adapters from 21 us to 25.  Fewer are level: 1024 rows of 64 adapters at rank 16, 1, 2 and 4 blocks
+    // 76, 78 and 79; 96 rows in one launch, 1 and 2 blocks 15.7 and 15.2.
+    static constexpr int kOwnBlocks = kSteps == 1 && !SELF ? 4 : 2;
     static constexpr int kMany = kDepth * (kB + kBase), kFew = kWaves * kOwnBlocks * kB;
-    static constexpr int kSelfDepth = RF == 1 ? 3 : 4;      // slices of multiply_alone()
+    // Slices of multiply_alone().  At rank 16 a fourth leaves one workgroup a CU: 96 rows of 64 adapters 19.5 us instead
+    // of 15.2, one row level.  At rank 32 there is one anyway: 16 rows of 16 adapters 9.3, with three 9.9.
+    static constexpr int kSelfDepth = RF == 1 ? 3 : 4;
     static constexpr int kPitch = 32 * kSteps + 8;          // bf16 values of a row of h: 16 rows in different banks
     static constexpr int kH = SELF ? 2 * 16 * kPitch * 2 : 0;
     // SELF: the first product's ring is free when products come, and holds them
@@ -737,7 +744,8 @@ int passes_of(int m, int adapters) {
 }
 
 // Passes that get workgroups of their own when the work is split.  In up to 4 tiles (a decode batch) any
-// row may have an adapter of its own, or all rows one; more rows are made of runs.  256 rows of 64 adapters
+// row may have an adapter of its own, or all rows one; more rows are taken to be runs, which costs where they are not:
+// 512 rows of 64 adapters in any order at rank 64 take 84 us, 512 of one run 21.  256 rows of 64 adapters
 // at rank 64, all different | all one (us): with 4 passes 58 | 22, 16 46 | 29, 64 47 | 87, so 64 in all tiles.
 int expected_passes(int m, int adapters) {
     const int most = passes_of(m, adapters), tiles = tiles_of(m);
@@ -755,8 +763,10 @@ int slots_of(int m, int adapters, int others) {
 int at_most(int v, int most) { return v < 1 || most < 1 ? 1 : v < most ? v : most; }
 
 // Workgroups that a kernel is split into: three quarters of the 512 that the chip holds (two a CU by their
-// LDS), so that the second passes of tiles that two runs share find room beside the first.  8192 rows at
-// rank 64, n = k = 4096, 8 runs: 58 us, with 256 or 512 instead 70 and 72.
+// LDS), so that the second passes of tiles that two runs share find room beside the first.  With 256 | 384 | 512 (us, n =
+// k = 4096, runs of 900 rows): 8192 rows at rank 64 75 | 61 | 76, at rank 16 61 | 50 | 61, at rank 128 105 | 91 | 115.  Fewer
+// rows would like 256: 4096 at rank 64 37 | 38 | 45, 2048 27 | 29 | 32, in runs of 100 29 | 35 | 35; the host does not see
+// runs.
 constexpr int kWorkgroups = 384;
 
 template <int RF>
@@ -767,8 +777,10 @@ void launch_shrink(const LoraArgs& a, hipStream_t s) {
 }
 
 // Multiples of 16 tiles, once some CUs get a second workgroup, run slower than their neighbours, which an
-// empty tile mends by making the number odd (measured; the cause is not known): 4096 rows at rank 64, n = 4096 |
-// 11008, 41 us | 68, without it 50 | 83.  Up to one workgroup a CU it costs: 16384 rows 127, without 122.
+// empty tile mends by making the number odd (measured; the cause is not known).  Without it | with it (us): rank 64, n =
+// 4096, 2048 rows 33 | 29, 4096 rows 43 | 38; n = 11008, 1024 rows 37 | 31, 2048 50 | 41, 4096 77 | 68; rank 128, 4096 rows, n
+// = 11008 116 | 99; rank 16 38 | 34.  At other numbers of tiles it costs where the sum becomes a multiple of 16 (4032 rows
+// at rank 64 41 | 46), and up to one workgroup a CU (1024 rows, n = 4096 22 | 25; 16384 138 | 142).
 template <int RF, bool SELF>
 void launch_out(const LoraArgs& a, int slots, int ranges, hipStream_t s) {
     const int tiles = tiles_of(a.m), empty = tiles % 16 == 0 && tiles * ranges > 256 ? 1 : 0;

@@ -18,7 +18,7 @@ namespace {
 // sums, so that a long prompt among short ones spreads over every thread of its chunk's slices.
 // What bounds it is the chain of dependent steps (lengths, sums, search, table or free list), not
 // bytes: one request 3.9 us on the device, 1024 requests of a token each 6.0, 97 prompts of 133 000
-// tokens in all 6.1 (1.6 MB of slots and rows), of which a launch is 2; the call takes 5.2 on the host.
+// tokens in all 6.1 (1.6 MB of slots and rows), of which a launch is 2; the call takes 6 to 7 on the host.
 // ---------------------------------------------------------------------------------------------
 constexpr int kPlanThreads = 256;
 
