@@ -155,7 +155,7 @@ def prepare(case, seed):
     width = n // 2 if gated else n
     return dict(case, a=codes, a_scale=a_scale, b=b, b_scale=b_scale,
                 bias=torch.randn(n, generator=g, device=DEV) if case["shift"] else None,
-                residual=torch.randn((m, n), generator=g, device=DEV).to(torch.bfloat16) if case["residual"] else None,
+                residual=torch.randn((m, n), generator=g, device=DEV).to(_dtype(case["out"])) if case["residual"] else None,
                 c=torch.empty((m, width), dtype=_dtype(case["out"]), device=DEV))
 
 
@@ -278,7 +278,7 @@ def work(case):
     size = 4 if case["out"] == "f32" else 2
     width = n if case["gate"] == "none" else n // 2
     return {"bytes": (m + n) * k + 4 * (m + _blocks(n)) * _blocks(k) + m * width * size
-            + (2 * m * n if case["residual"] else 0) + (4 * n if case["shift"] else 0), "flops": 2 * m * n * k}
+            + (size * m * n if case["residual"] else 0) + (4 * n if case["shift"] else 0), "flops": 2 * m * n * k}
 
 
 # ----------------------------------------------------------------------------------------------
