@@ -42,22 +42,22 @@ def listed():
         dict(name="quantise prompts", op="quant", rows=8192, cols=11008, wide=0, dtype="bf16"),
         # one user's token through an output projection: the weights are read once
         dict(name="product one token", op="product", m=1, n=4096, k=4096, gate="none", act="none", shift=False,
-             residual=True, out="bf16"),
+             residual=True),
         # a decode batch through gate and up projections
         dict(name="product decode gated", op="product", m=64, n=22016, k=4096, gate="silu", act="none", shift=False,
-             residual=False, out="bf16"),
+             residual=False),
         # and back through the down projection: few columns, a long sum
         dict(name="product decode down", op="product", m=64, n=4096, k=11008, gate="none", act="none", shift=False,
-             residual=True, out="bf16"),
+             residual=True),
         # a short prompt, sizes that end inside tiles and blocks, bias and GELU
         dict(name="product ragged", op="product", m=777, n=5000, k=4112, gate="none", act="gelu_tanh", shift=True,
-             residual=False, out="bf16"),
+             residual=False),
         # prompts through gate and up projections: the matrix cores' rate
         dict(name="product prompts gated", op="product", m=8192, n=22016, k=4096, gate="silu", act="none", shift=False,
-             residual=False, out="bf16"),
+             residual=False),
         # and back
         dict(name="product prompts down", op="product", m=8192, n=4096, k=11008, gate="none", act="none", shift=False,
-             residual=True, out="bf16"),
+             residual=True),
     ]
 
 
@@ -85,8 +85,7 @@ def draw(rng):
         m, n = max(1, m * 3 // 4), max(2, n * 3 // 8 * 2)
     plain = gate == "none"
     return dict(op=op, m=m, n=n, k=k, gate=gate, act=rng.choice(["none", "none", "relu", "gelu_tanh", "gelu_erf"]) if plain
-                else "none", shift=rng.random() < 0.4, residual=plain and rng.random() < 0.5,
-                out=rng.choice(["bf16", "bf16", "f32"]) if plain else "bf16")
+                else "none", shift=rng.random() < 0.4, residual=plain and rng.random() < 0.5)
 
 
 # ----------------------------------------------------------------------------------------------
@@ -155,8 +154,8 @@ def prepare(case, seed):
     width = n // 2 if gated else n
     return dict(case, a=codes, a_scale=a_scale, b=b, b_scale=b_scale,
                 bias=torch.randn(n, generator=g, device=DEV) if case["shift"] else None,
-                residual=torch.randn((m, n), generator=g, device=DEV).to(_dtype(case["out"])) if case["residual"] else None,
-                c=torch.empty((m, width), dtype=_dtype(case["out"]), device=DEV))
+                residual=torch.randn((m, n), generator=g, device=DEV).to(torch.bfloat16) if case["residual"] else None,
+                c=torch.empty((m, width), dtype=torch.bfloat16, device=DEV))
 
 
 # ----------------------------------------------------------------------------------------------
@@ -237,7 +236,7 @@ def _own(s):
         dlf.dlf_quant_blocks(d, s["x"], s["y"], s["scale"])
         return
     if d is None:
-        d = s["desc"] = dlf.gemm_blocks_desc(s["m"], s["n"], s["k"], s["out"], s["act"])
+        d = s["desc"] = dlf.gemm_blocks_desc(s["m"], s["n"], s["k"], s["act"])
         s["ws"] = torch.empty(dlf.dlf_gemm_blocks_workspace_bytes(d), dtype=torch.uint8, device=DEV)
     if s["gate"] != "none":
         dlf.dlf_gemm_blocks_gated(d, s["a"], s["a_scale"], s["b"], s["b_scale"], s["bias"], s["gate"], s["c"], s["ws"],
@@ -275,10 +274,9 @@ def work(case):
         return {"bytes": moved + (4 * cols if case["op"] == "norm" else 0),
                 "flops": rows * cols * (5 if case["op"] == "norm" else 2)}
     m, n, k = case["m"], case["n"], case["k"]
-    size = 4 if case["out"] == "f32" else 2
     width = n if case["gate"] == "none" else n // 2
-    return {"bytes": (m + n) * k + 4 * (m + _blocks(n)) * _blocks(k) + m * width * size
-            + (size * m * n if case["residual"] else 0) + (4 * n if case["shift"] else 0), "flops": 2 * m * n * k}
+    return {"bytes": (m + n) * k + 4 * (m + _blocks(n)) * _blocks(k) + 2 * m * width
+            + (2 * m * n if case["residual"] else 0) + (4 * n if case["shift"] else 0), "flops": 2 * m * n * k}
 
 
 # ----------------------------------------------------------------------------------------------
