@@ -128,6 +128,50 @@ def lora_desc(m, n, k, rank, adapters, requests=0, x_stride=None, base_stride=No
                          DTYPES.get(dtype, dtype))
 
 
+DLF_SCALE_BLOCK = 128
+
+
+def scale_stride(cols):
+    """Floats between two rows of block scales that lie close: one a 128 columns, rounded up to a multiple of 4."""
+    return -(-cols // (4 * DLF_SCALE_BLOCK)) * 4
+
+
+class dlf_rms_norm_desc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int32), ("scale_stride", ctypes.c_int32),
+                ("x_stride", ctypes.c_int64), ("residual_stride", ctypes.c_int64), ("sum_stride", ctypes.c_int64),
+                ("y_stride", ctypes.c_int64), ("dtype", ctypes.c_int), ("out_dtype", ctypes.c_int),
+                ("eps", ctypes.c_float), ("out_inv_scale", ctypes.c_float)]
+
+
+def rms_norm_desc(rows, cols, eps=1e-5, dtype="bf16", out_dtype="bf16", out_inv_scale=1.0, x_stride=None,
+                  residual_stride=None, sum_stride=None, y_stride=None, y_scale_stride=None):
+    strides = [cols if s is None else s for s in (x_stride, residual_stride, sum_stride, y_stride)]
+    return dlf_rms_norm_desc(rows, cols, scale_stride(cols) if y_scale_stride is None else y_scale_stride, *strides,
+                             DTYPES.get(dtype, dtype), DTYPES.get(out_dtype, out_dtype), eps, out_inv_scale)
+
+
+class dlf_quant_blocks_desc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int32), ("scale_stride", ctypes.c_int32),
+                ("x_stride", ctypes.c_int64), ("codes_stride", ctypes.c_int64), ("dtype", ctypes.c_int)]
+
+
+def quant_blocks_desc(rows, cols, dtype="bf16", x_stride=None, codes_stride=None, row_scale_stride=None):
+    return dlf_quant_blocks_desc(rows, cols, scale_stride(cols) if row_scale_stride is None else row_scale_stride,
+                                 cols if x_stride is None else x_stride,
+                                 cols if codes_stride is None else codes_stride, DTYPES.get(dtype, dtype))
+
+
+class dlf_gemm_blocks_desc(ctypes.Structure):
+    _fields_ = [("m", ctypes.c_int64), ("n", ctypes.c_int32), ("k", ctypes.c_int32),
+                ("a_scale_stride", ctypes.c_int32), ("b_scale_stride", ctypes.c_int32), ("act", ctypes.c_int)]
+
+
+def gemm_blocks_desc(m, n, k, act="none", a_scale_stride=None, b_scale_stride=None):
+    close = scale_stride(k)
+    return dlf_gemm_blocks_desc(m, n, k, close if a_scale_stride is None else a_scale_stride,
+                                close if b_scale_stride is None else b_scale_stride, ACTS.get(act, act))
+
+
 class dlf_graph_node(ctypes.Structure):
     _fields_ = [("op", ctypes.c_int32), ("n_inputs", ctypes.c_int32), ("inputs", ctypes.c_int32 * 2),
                 ("dtype", ctypes.c_int32), ("flags", ctypes.c_uint32), ("rank", ctypes.c_int32),
@@ -169,6 +213,13 @@ _SIGS = {
     "dlf_paged_attention": [ctypes.POINTER(dlf_paged_attn_desc)] + [_vp] * 8 + [ctypes.c_size_t, _vp],
     "dlf_lora_workspace_bytes": [ctypes.POINTER(dlf_lora_desc), ctypes.POINTER(ctypes.c_size_t)],
     "dlf_lora_add": [ctypes.POINTER(dlf_lora_desc)] + [_vp] * 9 + [ctypes.c_size_t, _vp],
+    "dlf_rms_norm": [ctypes.POINTER(dlf_rms_norm_desc)] + [_vp] * 7,
+    "dlf_quant_blocks": [ctypes.POINTER(dlf_quant_blocks_desc)] + [_vp] * 4,
+    "dlf_gemm_blocks_workspace_bytes": [ctypes.POINTER(dlf_gemm_blocks_desc), ctypes.POINTER(ctypes.c_size_t)],
+    "dlf_gemm_blocks": [ctypes.POINTER(dlf_gemm_blocks_desc)] + [_vp] * 8 + [ctypes.c_size_t, _vp],
+    "dlf_gemm_blocks_gated": [ctypes.POINTER(dlf_gemm_blocks_desc)] + [_vp] * 5 + [ctypes.c_int, _vp, _vp,
+                                                                                   ctypes.c_size_t, _vp],
+    "dlf_quant_blocks_weights": [_i64, _i64, _vp, ctypes.c_int32, ctypes.c_int32, _vp, _vp],
     "dlf_clock_probe": [ctypes.c_int32, ctypes.c_int32, _vp, _vp],
     "dlf_fusion_plan": [ctypes.POINTER(dlf_graph_node), ctypes.c_int32, ctypes.c_double, ctypes.c_double,
                         ctypes.POINTER(dlf_fusion_group), ctypes.c_int32, ctypes.POINTER(ctypes.c_int32)],
@@ -516,6 +567,103 @@ def dlf_lora_add(desc, x, a, b, scale, ids, row_map, base, out, workspace, works
                              _sized(row_map, _I32, 4 * m, "row_map"), _matrix(base, m, n, desc.base_stride, "base"),
                              _matrix(out, m, n, desc.out_stride, "out"), _workspace(workspace, workspace_bytes),
                              workspace_bytes, _stream(stream)), "dlf_lora_add")
+
+
+_TYPES = {DLF_F32: (_F32, 4), DLF_BF16: (_BF16, 2), DLF_FP8_E4M3: (_FP8, 1)}
+
+
+def _strided(t, dtype, rows, cols, stride, name):
+    """Device pointer of a [rows][cols] tensor of the descriptor's type whose rows are `stride` elements apart,
+    or of a raw address or None as it is."""
+    if t is None or isinstance(t, int):
+        return t
+    want = _TYPES.get(dtype, (None, 0))[0]      # an unknown type is the library's to refuse
+    if want is not None and t.dtype is not want and t.dtype not in _BITS.get(want, ()):
+        raise ValueError(f"{name} has type {t.dtype}, {want} is needed")
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 2 or shape[0] != rows or shape[1] != cols or (cols > 1 and strides[1] != 1) or (
+            rows > 1 and cols > 0 and strides[0] != stride):
+        raise ValueError(f"{name} must be [{rows}][{cols}] with rows {stride} elements apart")
+    return t.data_ptr()
+
+
+def _scales(t, rows, blocks, stride, name):
+    """Device pointer of contiguous fp32 block scales, `rows` rows of `stride` values (after the last row's last
+    scale nothing is needed), or of a raw address or None as it is."""
+    return _sized(t, _F32, 4 * ((rows - 1) * stride + blocks) if rows > 0 else 0, name)
+
+
+def dlf_rms_norm(desc, x, residual, weight, sum, y, y_scale, stream=None):
+    """y = norm(x + residual) * weight, and the sum itself (see include/dlfusion.h); the rows lie the descriptor's
+    strides apart."""
+    n, cols, dtype = desc.rows, desc.cols, desc.dtype
+    _check(_lib.dlf_rms_norm(ctypes.byref(desc), _strided(x, dtype, n, cols, desc.x_stride, "x"),
+                             _strided(residual, dtype, n, cols, desc.residual_stride, "residual"),
+                             _sized(weight, _F32, 4 * cols, "weight"),
+                             _strided(sum, dtype, n, cols, desc.sum_stride, "sum"),
+                             _strided(y, desc.out_dtype, n, cols, desc.y_stride, "y"),
+                             _scales(y_scale, n, -(-cols // 128), desc.scale_stride, "y_scale"), _stream(stream)),
+           "dlf_rms_norm")
+
+
+def dlf_quant_blocks(desc, x, codes, scale, stream=None):
+    """Rows as e4m3 codes and a scale for each 128 columns (see include/dlfusion.h)."""
+    n, cols = desc.rows, desc.cols
+    _check(_lib.dlf_quant_blocks(ctypes.byref(desc), _strided(x, desc.dtype, n, cols, desc.x_stride, "x"),
+                                 _strided(codes, DLF_FP8_E4M3, n, cols, desc.codes_stride, "codes"),
+                                 _scales(scale, n, -(-cols // 128), desc.scale_stride, "scale"), _stream(stream)),
+           "dlf_quant_blocks")
+
+
+def dlf_gemm_blocks_workspace_bytes(desc):
+    n = ctypes.c_size_t(0)
+    _check(_lib.dlf_gemm_blocks_workspace_bytes(ctypes.byref(desc), ctypes.byref(n)), "dlf_gemm_blocks_workspace_bytes")
+    return n.value
+
+
+def _gemm_blocks_operands(desc, a, a_scale, b, b_scale, col_shift, slabs):
+    m, n, k = desc.m, desc.n, desc.k
+    blocks = -(-k // 128)
+    return (_strided(a, DLF_FP8_E4M3, m, k, k, "a"), _scales(a_scale, m, blocks, desc.a_scale_stride, "a_scale"),
+            _strided(b, DLF_FP8_E4M3, n, k, k, "b"), _scales(b_scale, slabs, blocks, desc.b_scale_stride, "b_scale"),
+            _sized(col_shift, _F32, 4 * n, "col_shift"))
+
+
+def dlf_gemm_blocks(desc, a, a_scale, b, b_scale, col_shift, residual, c, workspace, workspace_bytes, stream=None):
+    """Product of e4m3 matrices whose rows have a scale for each 128 values of k, b's for each 128 rows
+    (see include/dlfusion.h)."""
+    m, n = desc.m, desc.n
+    workspace_bytes = int(workspace_bytes)
+    _check(_lib.dlf_gemm_blocks(ctypes.byref(desc),
+                                *_gemm_blocks_operands(desc, a, a_scale, b, b_scale, col_shift, -(-n // 128)),
+                                _strided(residual, DLF_BF16, m, n, n, "residual"),
+                                _strided(c, DLF_BF16, m, n, n, "c"),
+                                _workspace(workspace, workspace_bytes), workspace_bytes, _stream(stream)),
+           "dlf_gemm_blocks")
+
+
+def dlf_gemm_blocks_gated(desc, a, a_scale, b, b_scale, col_shift, gate, c, workspace, workspace_bytes, stream=None):
+    """The same with interleaved gate and up rows: c[:, j] = gate(g_j) * u_j."""
+    m, n = desc.m, desc.n
+    workspace_bytes = int(workspace_bytes)
+    _check(_lib.dlf_gemm_blocks_gated(ctypes.byref(desc),
+                                      *_gemm_blocks_operands(desc, a, a_scale, b, b_scale, col_shift, 2 * -(-n // 256)),
+                                      GATES.get(gate, gate), _strided(c, DLF_BF16, m, n // 2, n // 2, "c"),
+                                      _workspace(workspace, workspace_bytes), workspace_bytes, _stream(stream)),
+           "dlf_gemm_blocks_gated")
+
+
+def dlf_quant_blocks_weights(w, gated=False):
+    """Host: fp32 weights [n][k] as e4m3 codes (uint8 [n][k]) and the scales of their 128 x 128 blocks (float32
+    [rows][scale_stride(k)]); gated: rows 2j and 2j + 1 are gate and up (see include/dlfusion.h)."""
+    arr, p = _host(w, np.float32)
+    n, k = arr.shape
+    stride = scale_stride(k)
+    codes = np.empty((n, k), dtype=np.uint8)
+    scale = np.empty((2 * -(-n // 256) if gated else -(-n // 128), stride), dtype=np.float32)
+    _check(_lib.dlf_quant_blocks_weights(n, k, p, int(gated), stride, codes.ctypes.data, scale.ctypes.data),
+           "dlf_quant_blocks_weights")
+    return codes, scale
 
 
 def dlf_clock_probe(workgroups, iters, stamps, stream=None):

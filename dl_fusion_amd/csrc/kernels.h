@@ -242,6 +242,49 @@ struct LoraArgs {
 int lora_parts(int m, int k, int rank, int adapters);
 hipError_t launch_lora(const LoraArgs& args, hipStream_t stream);
 
+// Root-mean-square norm of rows (dlf_rms_norm).
+struct RmsNormArgs {
+    const void* x;              // [rows][cols], fp32 or bf16
+    const void* residual;       // nullable
+    const float* weight;        // [cols] or nullptr (= 1)
+    void* sum;                  // nullable
+    void* y;
+    float* scale;               // [rows][scale_stride], block scales of an e4m3 y, or nullptr
+    int64_t rows;               // < 2^31
+    int64_t x_stride, residual_stride, sum_stride, y_stride;
+    int cols, scale_stride;
+    float eps, inv_scale;
+};
+// out: kOutBf16 / kOutF32 / kOutFp8 (block scales where scale is given, else inv_scale)
+hipError_t launch_rms_norm(const RmsNormArgs& args, bool f32, int out, hipStream_t stream);
+
+// Rows into e4m3 codes with a scale for each 128 columns (dlf_quant_blocks).
+struct QuantBlocksArgs {
+    const void* x;              // [rows][cols], fp32 or bf16
+    uint8_t* codes;
+    float* scale;               // [rows][scale_stride]
+    int64_t x_stride, codes_stride;
+    uint32_t blocks;            // of all rows, < 2^31
+    int cols, row_blocks, scale_stride;
+};
+hipError_t launch_quant_blocks(const QuantBlocksArgs& args, bool f32, hipStream_t stream);
+
+// Product of e4m3 matrices with block scales (dlf_gemm_blocks, dlf_gemm_blocks_gated).
+struct GemmBlocksArgs {
+    const uint8_t* a;           // [m][k]
+    const float* a_scale;       // [m][a_scale_stride]
+    const uint8_t* b;           // [n][k]
+    const float* b_scale;       // [ceil(n / 128)][b_scale_stride]; gated: [2 ceil(n / 256)]
+    const float* shift;         // [n] or nullptr
+    const uint16_t* residual;   // [m][n] or nullptr
+    uint16_t* c;                // [m][n]; gated: [m][n / 2]
+    int64_t m;
+    int n, k;
+    int a_scale_stride, b_scale_stride;
+};
+// act: kAct*, or kActSiluMul.. for the gated form
+hipError_t launch_gemm_blocks(const GemmBlocksArgs& args, int act, hipStream_t stream);
+
 // Shader-clock probe: workgroups x 4 waves of back-to-back bf16 MFMAs; stamps[4 b + 0..3] =
 // s_memtime before / after, s_memrealtime before / after, for workgroup b.
 hipError_t launch_clock_probe(int workgroups, int iters, uint64_t* stamps, hipStream_t stream);

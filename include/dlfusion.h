@@ -383,6 +383,149 @@ dlf_status dlf_ffn_fused_noalloc(const dlf_ffn_desc *d, const void *x, const voi
                                  const void *residual, void *y, void *stream);
 
 /* ---------------------------------------------------------------------- */
+/* 8-bit products whose scales follow the data                              */
+/* ---------------------------------------------------------------------- */
+
+/* A static per-tensor scale (dlf_gemm_fused on e4m3) has to hold the largest
+ * value that a tensor will ever have.  Here a row of activations has a scale
+ * for each DLF_SCALE_BLOCK columns, found as the row is written, and a weight
+ * one for each DLF_SCALE_BLOCK x DLF_SCALE_BLOCK values:
+ *     dlf_rms_norm      a norm whose output may be such codes and scales
+ *     dlf_quant_blocks  any rows (an attention's or a gate's output) into them
+ *     dlf_gemm_blocks, dlf_gemm_blocks_gated   the products
+ *     dlf_quant_blocks_weights   weights into that form, on the host, at load
+ * The last block of a row may be short.  A block of values v becomes
+ *     amax  = max(2^-110, max |v| over its finite v)
+ *     scale = fp32(amax / 448)
+ *     code  = Q( fp32(v * fp32(448 / amax)) )
+ * with the quantiser Q of the fp8 GEMM (nearest, ties to even, saturating at
+ * +-448), except that a NaN stays a NaN: an infinity is the block's largest value,
+ * and takes nothing from the others'.  Scales of activations lie
+ * [rows][scale_stride] fp32, block b of a row at b; scale_stride is a multiple of
+ * 4, so that the scales of four blocks are one load, and what lies between a
+ * row's last scale and the next row is neither read for its value nor written. */
+#define DLF_SCALE_BLOCK 128
+
+/* Sizes and types of a norm.  Strides are elements between rows, at least
+ * cols; those of tensors that are not given are not looked at. */
+typedef struct {
+    int64_t rows;
+    int32_t cols;               /* 1 .. 2^23 */
+    int32_t scale_stride;       /* with y_scale: >= ceil(cols / 128), a multiple of 4 */
+    int64_t x_stride, residual_stride, sum_stride, y_stride;
+    dlf_dtype dtype;            /* x, residual and sum: BF16 or F32 */
+    dlf_dtype out_dtype;        /* y: BF16, F32 or FP8_E4M3 */
+    float eps;                  /* finite, > 0 */
+    float out_inv_scale;        /* FP8_E4M3 without y_scale: fp32(1 / s_y), finite and > 0 */
+} dlf_rms_norm_desc;
+
+/* Root-mean-square norm of rows, with the addition of a residual before it:
+ *     h   = x [+ residual]
+ *     sum = h, rounded once
+ *     y   = h / sqrt(mean(h^2) + eps) * weight
+ * in fp32, y from h as it was before sum's rounding, and rounded once: to bf16,
+ * to e4m3 by a static scale, Q(fp32(y * out_inv_scale)), for dlf_gemm_fused, or,
+ * with y_scale, to codes and block scales, for dlf_gemm_blocks (a NaN stays a NaN
+ * in both).  A row whose sum of squares passes fp32's range is summed again 2^-80
+ * times as large; the order of a row's sum depends on cols alone.  As the formula
+ * has it, an infinity in a row becomes a NaN there and the other values 0, and a
+ * NaN makes the whole row NaN.
+ *   x         device [rows][cols], rows x_stride apart
+ *   residual  the same type, or NULL (= 0)
+ *   weight    device [cols] fp32 or NULL (= 1)
+ *   sum       device [rows][cols] of d->dtype, or NULL (not stored)
+ *   y         device [rows][cols] of d->out_dtype
+ *   y_scale   device [rows][scale_stride] fp32, or NULL; FP8_E4M3 only
+ * Rows may start at any element (odd widths and strides cost 10 to 40%, see the
+ * kernel); the tensors themselves are 16-byte aligned.  sum, and y where it has the
+ * inputs' type, may be x or residual itself, with its stride: a residual stream is
+ * updated in place.  Any other overlap of the tensors' ranges, from first element
+ * to last: DLF_ERR_ALIAS.  UNSUPPORTED: another type, cols above 2^23, 2^31 or more
+ * rows, strides above 2^31, a scale_stride that is no multiple of 4. */
+dlf_status dlf_rms_norm(const dlf_rms_norm_desc *d, const void *x, const void *residual,
+                        const float *weight, void *sum, void *y, float *y_scale, void *stream);
+
+typedef struct {
+    int64_t rows;
+    int32_t cols;               /* 1 .. 2^23 */
+    int32_t scale_stride;       /* >= ceil(cols / 128), a multiple of 4 */
+    int64_t x_stride, codes_stride;     /* elements between rows, >= cols */
+    dlf_dtype dtype;            /* x: BF16 or F32 */
+} dlf_quant_blocks_desc;
+
+/* Rows of values as e4m3 codes and block scales, as defined above.
+ *   x         device [rows][cols] of d->dtype, rows x_stride apart
+ *   codes     device uint8 [rows][cols], rows codes_stride apart
+ *   scale     device fp32 [rows][scale_stride]
+ * Alignment, overlaps and UNSUPPORTED as in dlf_rms_norm; further UNSUPPORTED:
+ * rows * ceil(cols / 128) of 2^31 or more. */
+dlf_status dlf_quant_blocks(const dlf_quant_blocks_desc *d, const void *x, uint8_t *codes,
+                            float *scale, void *stream);
+
+/* Sizes of a product of e4m3 matrices with block scales; its output is bf16. */
+typedef struct {
+    int64_t m;
+    int32_t n, k;               /* k a multiple of 16; both at most 2^23 */
+    int32_t a_scale_stride, b_scale_stride;     /* floats between rows of scales: multiples of 4,
+                                 * >= ceil(k / 128) */
+    dlf_act act;
+} dlf_gemm_blocks_desc;
+
+/* Bytes of device workspace dlf_gemm_blocks and dlf_gemm_blocks_gated need
+ * for d, written to *bytes: where the outputs alone would leave CUs idle, the sum
+ * over k is cut into parts and joined.  The descriptor checks and statuses of
+ * dlf_gemm_blocks; bytes NULL: DLF_ERR_INVALID_ARG.  Host only. */
+dlf_status dlf_gemm_blocks_workspace_bytes(const dlf_gemm_blocks_desc *d, size_t *bytes);
+
+/* The matrix product of dlf_gemm_fused for operands with block scales:
+ *     acc[i][j] = sum over blocks t of k of
+ *                 a_scale[i][t] * b_scale[j / 128][t] * sum over k in t of a[i][k] b[j][k]
+ *     c[i][j]   = act( acc[i][j] + col_shift[j] [+ residual[i][j]] )
+ * The blocks' sums are added in fp32, c is rounded once.  Inside a block the matrix
+ * cores cut each product of two codes 2^-14 below the largest of its neighbours
+ * (measured: 2e-6 of sum |a b| on normal values, against the 2^-9 of c's own rounding).
+ * The order of the sums depends on the descriptor alone: the same inputs give the
+ * same bits.
+ *   a, a_scale   device e4m3 [m][k] and fp32 [m][a_scale_stride]
+ *   b, b_scale   device e4m3 [n][k] and fp32 [ceil(n / 128)][b_scale_stride]
+ *   col_shift    device [n] fp32 or NULL (= 0)
+ *   residual     device bf16 [m][n] or NULL
+ *   c            device bf16 [m][n]
+ *   workspace    device, 16-byte aligned, at least
+ *                dlf_gemm_blocks_workspace_bytes(d) bytes, overlapping no operand;
+ *                may be NULL where that size is 0.  Scratch: calls that share one on
+ *                overlapping streams race
+ * UNSUPPORTED: k % 16 != 0, n or k above 2^23, m above 2^24, a scale stride that
+ * is no multiple of 4, m * n of 2^38 or more. */
+dlf_status dlf_gemm_blocks(const dlf_gemm_blocks_desc *d, const void *a, const float *a_scale,
+                           const void *b, const float *b_scale, const float *col_shift,
+                           const void *residual, void *c, void *workspace,
+                           size_t workspace_bytes, void *stream);
+
+/* The gated projection of dlf_gemm_fused_gated for such operands: b row 2j is
+ * gate weight j, row 2j+1 up weight j, and
+ *     c[i][j] = gate(g) * u,  g and u = acc + col_shift of columns 2j and 2j+1,
+ * c [m][n/2].  The 128 gate rows and the 128 up rows of 256 neighbours keep the
+ * scales that they had before they were interleaved: row r of b has
+ *     b_scale[2 (r / 256) + r % 2],   b_scale [2 ceil(n / 256)][b_scale_stride].
+ * n even and d->act NONE, else DLF_ERR_INVALID_ARG; otherwise as dlf_gemm_blocks. */
+dlf_status dlf_gemm_blocks_gated(const dlf_gemm_blocks_desc *d, const void *a, const float *a_scale,
+                                 const void *b, const float *b_scale, const float *col_shift,
+                                 dlf_gate gate, void *c, void *workspace, size_t workspace_bytes,
+                                 void *stream);
+
+/* Weights for the products: w fp32 [n][k], as e4m3 codes [n][k] and the scales
+ * of its 128 x 128 blocks, [ceil(n / 128)][scale_stride] fp32; with `gated`, w holds
+ * gate and up rows interleaved and the scales' rows are those of
+ * dlf_gemm_blocks_gated.  amax as in the blocks of a row; scale =
+ * fp32(amax / 448) and code = Q(w / scale) in binary64, each rounded once (no
+ * double rounding).  Weights have to be finite (else DLF_ERR_INVALID_ARG, nothing
+ * written).  What lies past a row's last scale is set to 0.  Host memory,
+ * synchronous; touches no GPU. */
+dlf_status dlf_quant_blocks_weights(int64_t n, int64_t k, const float *w, int32_t gated,
+                                    int32_t scale_stride, uint8_t *codes, float *scale);
+
+/* ---------------------------------------------------------------------- */
 /* Decoding over a paged key-value cache                                    */
 /* ---------------------------------------------------------------------- */
 
