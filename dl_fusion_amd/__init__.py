@@ -587,10 +587,9 @@ def _strided(t, dtype, rows, cols, stride, name):
     return t.data_ptr()
 
 
-def _scales(t, rows, blocks, stride, name):
-    """Device pointer of contiguous fp32 block scales, `rows` rows of `stride` values (after the last row's last
-    scale nothing is needed), or of a raw address or None as it is."""
-    return _sized(t, _F32, 4 * ((rows - 1) * stride + blocks) if rows > 0 else 0, name)
+def _scales(t, rows, stride, name):
+    """Device pointer of contiguous fp32 block scales [rows][stride], or of a raw address or None as it is."""
+    return _sized(t, _F32, 4 * rows * stride, name)
 
 
 def dlf_rms_norm(desc, x, residual, weight, sum, y, y_scale, stream=None):
@@ -602,7 +601,7 @@ def dlf_rms_norm(desc, x, residual, weight, sum, y, y_scale, stream=None):
                              _sized(weight, _F32, 4 * cols, "weight"),
                              _strided(sum, dtype, n, cols, desc.sum_stride, "sum"),
                              _strided(y, desc.out_dtype, n, cols, desc.y_stride, "y"),
-                             _scales(y_scale, n, -(-cols // 128), desc.scale_stride, "y_scale"), _stream(stream)),
+                             _scales(y_scale, n, desc.scale_stride, "y_scale"), _stream(stream)),
            "dlf_rms_norm")
 
 
@@ -611,7 +610,7 @@ def dlf_quant_blocks(desc, x, codes, scale, stream=None):
     n, cols = desc.rows, desc.cols
     _check(_lib.dlf_quant_blocks(ctypes.byref(desc), _strided(x, desc.dtype, n, cols, desc.x_stride, "x"),
                                  _strided(codes, DLF_FP8_E4M3, n, cols, desc.codes_stride, "codes"),
-                                 _scales(scale, n, -(-cols // 128), desc.scale_stride, "scale"), _stream(stream)),
+                                 _scales(scale, n, desc.scale_stride, "scale"), _stream(stream)),
            "dlf_quant_blocks")
 
 
@@ -623,9 +622,8 @@ def dlf_gemm_blocks_workspace_bytes(desc):
 
 def _gemm_blocks_operands(desc, a, a_scale, b, b_scale, col_shift, slabs):
     m, n, k = desc.m, desc.n, desc.k
-    blocks = -(-k // 128)
-    return (_strided(a, DLF_FP8_E4M3, m, k, k, "a"), _scales(a_scale, m, blocks, desc.a_scale_stride, "a_scale"),
-            _strided(b, DLF_FP8_E4M3, n, k, k, "b"), _scales(b_scale, slabs, blocks, desc.b_scale_stride, "b_scale"),
+    return (_strided(a, DLF_FP8_E4M3, m, k, k, "a"), _scales(a_scale, m, desc.a_scale_stride, "a_scale"),
+            _strided(b, DLF_FP8_E4M3, n, k, k, "b"), _scales(b_scale, slabs, desc.b_scale_stride, "b_scale"),
             _sized(col_shift, _F32, 4 * n, "col_shift"))
 
 

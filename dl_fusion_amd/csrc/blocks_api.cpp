@@ -94,7 +94,7 @@ extern "C" dlf_status dlf_rms_norm(const dlf_rms_norm_desc* d, const void* x, co
     const Span ws{weight, static_cast<size_t>(d->cols) * 4};
     const Span ss{sum, rows_bytes(d->rows, d->sum_stride, d->cols, size)};
     const Span ys{y, rows_bytes(d->rows, d->y_stride, d->cols, size_of(d->out_dtype))};
-    const Span cs{y_scale, rows_bytes(d->rows, d->scale_stride, blocks_of(d->cols), 4)};
+    const Span cs{y_scale, rows_bytes(d->rows, d->scale_stride, d->scale_stride, 4)};
     // an output that is an input itself: each element is written by the thread that has read it
     auto itself = [&](const void* out, int64_t stride, const void* in, int64_t in_stride) {
         return out == in && stride == in_stride;
@@ -140,7 +140,7 @@ extern "C" dlf_status dlf_quant_blocks(const dlf_quant_blocks_desc* d, const voi
     if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scale, 16))
         return fail(DLF_ERR_INVALID_ARG, "device pointers must be 16-byte aligned");
     if (any_overlap({{codes, rows_bytes(d->rows, d->codes_stride, d->cols, 1)},
-                     {scale, rows_bytes(d->rows, d->scale_stride, blocks_of(d->cols), 4)}},
+                     {scale, rows_bytes(d->rows, d->scale_stride, d->scale_stride, 4)}},
                     {{x, rows_bytes(d->rows, d->x_stride, d->cols, size_of(d->dtype))}}))
         return fail(DLF_ERR_ALIAS, "an output overlaps an input or another output");
     dlf::QuantBlocksArgs a{};
@@ -191,8 +191,8 @@ dlf_status run_gemm(const dlf_gemm_blocks_desc* d, const void* a, const float* a
     const size_t m = static_cast<size_t>(d->m), n = static_cast<size_t>(d->n), k = static_cast<size_t>(d->k);
     const int64_t slabs = gated ? 2 * ((d->n + 2 * dlf::kScaleBlock - 1) / (2 * dlf::kScaleBlock)) : blocks_of(d->n);
     const Span cs{c, m * (gated ? n / 2 : n) * 2}, ws{workspace, need};
-    if (any_overlap({cs, ws}, {{a, m * k}, {b, n * k}, {a_scale, rows_bytes(d->m, d->a_scale_stride, blocks_of(d->k), 4)},
-                               {b_scale, rows_bytes(slabs, d->b_scale_stride, blocks_of(d->k), 4)}, {shift, n * 4},
+    if (any_overlap({cs, ws}, {{a, m * k}, {b, n * k}, {a_scale, rows_bytes(d->m, d->a_scale_stride, d->a_scale_stride, 4)},
+                               {b_scale, rows_bytes(slabs, d->b_scale_stride, d->b_scale_stride, 4)}, {shift, n * 4},
                                {residual, m * n * 2}}))
         return fail(DLF_ERR_ALIAS, "the output or the workspace overlaps an operand");
     dlf::GemmBlocksArgs g{};

@@ -402,8 +402,9 @@ dlf_status dlf_ffn_fused_noalloc(const dlf_ffn_desc *d, const void *x, const voi
  * +-448), except that a NaN stays a NaN: an infinity is the block's largest value,
  * and takes nothing from the others'.  Scales of activations lie
  * [rows][scale_stride] fp32, block b of a row at b; scale_stride is a multiple of
- * 4, so that the scales of four blocks are one load, and what lies between a
- * row's last scale and the next row is neither read for its value nor written. */
+ * 4, so that the scales of four blocks are one load.  The entries after a row's last
+ * scale are there in every row, the last one too; their values are not used, and
+ * nothing is written to them. */
 #define DLF_SCALE_BLOCK 128
 
 /* Sizes and types of a norm.  Strides are elements between rows, at least
