@@ -24,10 +24,15 @@ struct BlockTile {
     static constexpr int NW = WM * WN, NT = 64 * NW;
     static constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW;    // 1 KB loads a wave and block of k
     static constexpr int kStage = (BM + BN) * kScaleBlock;      // bytes of a block of k
-    static constexpr int kScales = BM * 16 + 1024;              // of four blocks' scales: a's rows, and two rows of b's
+    // scales in LDS, kGroup blocks of k at a time: of a's rows, in the order in which a lane wants them, the same row of
+    // four fragments together; and of two rows of b's
+    static constexpr int kGroup = 8;
+    static constexpr int H = (FM + 3) / 4;
+    static constexpr int kARow = WM * H * 64;                   // floats of a block
+    static constexpr int kScales = (kGroup * kARow + 2 * kGroup) * 4;
     static constexpr int kOut = BM * BN * 2;                    // the staged output
     static constexpr int kLds = 2 * kStage + 2 * kScales > kOut ? 2 * kStage + 2 * kScales : kOut;
-    static_assert(FM % 2 == 0, "two buffers in turn");
+    static_assert(FM % 4 == 0 && (LA + LB) % 8 == 0, "fragments and loads in turn");
     static_assert(LA >= 1 && LB >= 1 && BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && NW % 2 == 0, "whole loads");
     static_assert(BM % 64 == 0 && (BN == 128 || BN == 256 || BN == 64), "scales of whole waves, at most two rows of b's");
 };
@@ -82,26 +87,42 @@ __global__ __launch_bounds__(T::NT, 2) void gemm_blocks_kernel(const GemmBlocksA
     const int slabs = GATED ? slab + 2 : (p.n + kScaleBlock - 1) / kScaleBlock;
     const __amdgpu_buffer_rsrc_t rsb = buffer_rsrc(p.b_scale + static_cast<int64_t>(slab) * p.b_scale_stride,
                                                    static_cast<uint32_t>((slabs - slab < 2 ? slabs - slab : 2) * p.b_scale_stride * 4));
-    uint8_t* const scales = lds + 2 * T::kStage;
-    auto load_block = [&](int t) {
+    float* const scales = reinterpret_cast<float*>(lds + 2 * T::kStage);
+    constexpr int kLoads = T::LA + T::LB;
+    // load q of this wave's of block t, whose offset is `off`; past the last block and past k: zeros
+    auto load_off = [&](int t) {
         const uint32_t at = static_cast<uint32_t>(t) * kScaleBlock;
-        const uint32_t off = static_cast<int>(at) + 16 * chunk < k ? from + at : kOutOfRange;
-        uint8_t* const to = lds + (t & 1) * T::kStage + wave * 1024;
-#pragma unroll
-        for (int j = 0; j < T::LA; ++j) load_lds16_buf(ra[j], off, to + j * T::NW * 1024);
-#pragma unroll
-        for (int j = 0; j < T::LB; ++j) load_lds16_buf(rb[j], off, to + T::BM * kScaleBlock + j * T::NW * 1024);
+        return static_cast<int>(at) + 16 * chunk < k ? from + at : kOutOfRange;
     };
-    // scales of blocks 4 u .. 4 u + 3, 16 bytes a row
-    auto load_scales = [&](int u) {
-        uint8_t* const to = scales + (u & 1) * T::kScales;
-        for (int q = wave; q <= T::BM / 64; q += T::NW) {
-            if (q < T::BM / 64)
-                load_lds16_buf(rsa, static_cast<uint32_t>(64 * q + lane) * static_cast<uint32_t>(p.a_scale_stride) * 4u + 16u * u, to + q * 1024);
-            else
-                load_lds16_buf(rsb, lane < 2 ? static_cast<uint32_t>(lane) * static_cast<uint32_t>(p.b_scale_stride) * 4u + 16u * u : kOutOfRange,
-                               to + T::BM * 16);
+    auto load_part = [&](int t, int q, uint32_t off) {
+        uint8_t* const to = lds + (t & 1) * T::kStage + wave * 1024;
+        if (q < T::LA) load_lds16_buf(ra[q < T::LA ? q : 0], off, to + q * T::NW * 1024);
+        else load_lds16_buf(rb[q < T::LA ? 0 : q - T::LA], off, to + T::BM * kScaleBlock + (q - T::LA) * T::NW * 1024);
+    };
+    // Scales of the blocks kGroup u ..: two lanes a row and 16 bytes a lane, through registers, since LDS wants them in
+    // another order.  What lies past a row's last block is never used.
+    constexpr int kMine = T::BM / T::NW;                        // rows of a wave
+    const int arow = wave * kMine + (lane >> 1);
+    const bool mine = lane < 2 * kMine;
+    u32x4_t next_a{0u, 0u, 0u, 0u};
+    uint32_t next_b = 0;
+    auto fetch_scales = [&](int u) {
+        const uint32_t at = static_cast<uint32_t>(u) * (T::kGroup * 4);
+        next_a = __builtin_amdgcn_raw_buffer_load_b128(
+            rsa, mine ? static_cast<uint32_t>(arow) * static_cast<uint32_t>(p.a_scale_stride) * 4u + at + 16u * (lane & 1) : kOutOfRange, 0, 0);
+        if (wave == 0)
+            next_b = __builtin_amdgcn_raw_buffer_load_b32(
+                rsb, lane < 2 * T::kGroup ? (lane / T::kGroup) * static_cast<uint32_t>(p.b_scale_stride) * 4u + at + 4u * (lane % T::kGroup) : kOutOfRange, 0, 0);
+    };
+    auto keep_scales = [&](int u) {
+        float* const to = scales + (u & 1) * (T::kScales / 4);
+        const int frag = arow >> 4, in_wave = frag % FM;
+        const int at = ((frag / FM) * T::H + (in_wave >> 2)) * 64 + 4 * (arow & 15) + (in_wave & 3);
+        if (mine) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) to[(4 * (lane & 1) + e) * T::kARow + at] = __uint_as_float(next_a[e]);
         }
+        if (wave == 0 && lane < 2 * T::kGroup) to[T::kGroup * T::kARow + lane] = __uint_as_float(next_b);
     };
     // operand reads: chunks g and 4 + g of row `row` of a fragment (a and b alike: any order of k does)
     const uint32_t lo = static_cast<uint32_t>(row * kScaleBlock + 16 * (g ^ (row >> 1))), hi = lo ^ 64u;
@@ -120,73 +141,96 @@ __global__ __launch_bounds__(T::NT, 2) void gemm_blocks_kernel(const GemmBlocksA
         for (int i = 0; i < FM; ++i) acc[j][i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
     if (blocks > 0) {
-        load_scales(0);
-        load_block(0);
-        load_block(1);
-        wait_vmcnt<T::LA + T::LB>();
+        fetch_scales(0);
+#pragma unroll
+        for (int q = 0; q < kLoads; ++q) load_part(0, q, load_off(0));
+        keep_scales(0);
+        fetch_scales(1);
+        wait_vmcnt<0>();
         barrier();
-        i32x8_t w[FN], x[2];
+#pragma unroll
+        for (int q = 0; q < kLoads / 2; ++q) load_part(1, q, load_off(1));
+        // Fragments of a are read DEPTH groups of MFMAs ahead
+        constexpr int DEPTH = 2, RING = 4;
+        i32x8_t w[FN], x[RING];
+        f32x4_t sa[T::H];                   // scales of the rows of four fragments
+        float b0, b1;                       // of the wave's columns, even and odd
         f32x4_t part[2][FN];
-        float s0[2], s1[2], b0, b1;         // scales of a fragment's rows times those of its columns, even and odd
-        // the scales' place of block t, and row `row` of fragment i of a's
-        auto scale_at = [&](int t) { return reinterpret_cast<const float*>(scales + ((t >> 2) & 1) * T::kScales) + (t & 3); };
-        const int srow = 4 * (wm * FM * 16 + row);
-        const int sb0 = 4 * T::BM + (GATED ? 0 : 4 * (wn * FN * 16 / kScaleBlock)), sb1 = GATED ? sb0 + 4 : sb0;
-        const float* sc = scale_at(0);
-        b0 = sc[sb0];
-        b1 = sc[sb1];
-        float sa = sc[srow];
+        const int b_at = T::kGroup * T::kARow + (GATED ? 0 : T::kGroup * (wn * FN * 16 / kScaleBlock));
+        const float* sc;                    // the scales of a block
+        auto scales_of = [&](int t) { sc = scales + (t / T::kGroup & 1) * (T::kScales / 4) + (t % T::kGroup) * T::kARow; };
+        auto read_sa = [&](int h) { sa[h] = *reinterpret_cast<const f32x4_t*>(sc + (wm * T::H + h) * 64 + 4 * row); };
+        auto read_b = [&](int t) {
+            const float* const from = scales + (t / T::kGroup & 1) * (T::kScales / 4) + b_at + t % T::kGroup;
+            b0 = from[0];
+            b1 = GATED ? from[T::kGroup] : b0;
+        };
+        scales_of(0);
+        read_sa(0);
+        read_b(0);
 #pragma unroll
         for (int j = 0; j < FN; ++j) w[j] = read(wb + j * 2048);
-        x[0] = read(xa);
+#pragma unroll
+        for (int i = 0; i < DEPTH; ++i) x[i] = read(xa + i * 2048);
 #pragma unroll
         for (int j = 0; j < FN; ++j) part[(FM - 1) & 1][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-        s0[(FM - 1) & 1] = s1[(FM - 1) & 1] = 0.0f;
-        auto add = [&](int i) {             // fragment i's block, into its sum
-#pragma unroll
-            for (int j = 0; j < FN; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[j][i][e] = fmaf(part[i & 1][j][e], e & 1 ? s1[i & 1] : s0[i & 1], acc[j][i][e]);
-        };
+        float s0 = 0.0f, s1 = 0.0f;         // of the group whose sums are added next
         for (int t = 0; t < blocks;) {
-            // the next four blocks' scales; those before last have been read by all.  (Outside the loop below, whose
-            // body has to stay free of branches: the sums are moved past them otherwise, and their registers spilled.)
-            load_scales((t >> 2) + 1);
-            const int end = t + 4 < blocks ? t + 4 : blocks;
+            // The next kGroup blocks' scales into LDS, where those before the present ones have been used by all, and the ones
+            // after on their way.  (Outside the loop below, whose body has to stay free of branches: the sums are moved
+            // past them otherwise, and their registers spilled.)
+            keep_scales(t / T::kGroup + 1);
+            fetch_scales(t / T::kGroup + 2);
+            const int end = t + T::kGroup < blocks ? t + T::kGroup : blocks;
 #pragma unroll 1
             for (; t < end; ++t) {
                 const int stage = (t & 1) * T::kStage, next = T::kStage - stage;
+                const uint32_t off = load_off(t + 1), off2 = load_off(t + 2);
 #pragma unroll
                 for (int i = 0; i < FM; ++i) {
-                    const float s = sa;
-                    if (i + 1 < FM) {
-                        x[(i + 1) & 1] = read(xa + stage + (i + 1) * 2048);
-                        sa = sc[srow + (i + 1) * 64];
-                    } else {
-                        // every wave has read its last of this block, and has the next one's loads: refill this one
+                    // A stage is left by all DEPTH groups before its block's end.  Half of its loads follow at once, half in
+                    // the next block's first groups: spread over the MFMAs no wave waits for room in the queue of loads.
+                    if (i < FM / 4) {
+#pragma unroll
+                        for (int q = 0; q < kLoads / (FM / 2); ++q) load_part(t + 1, kLoads / 2 + i * (kLoads / (FM / 2)) + q, off);
+                    }
+                    if (i + DEPTH == FM) {
+                        // this wave's loads of the next block are there and its reads of this one done; after the barrier
+                        // everyone's are
                         wait_vmcnt<0>();
                         barrier();
-                        load_block(t + 2);
-                        x[(i + 1) & 1] = read(xa + next);
                     }
-                    s0[i & 1] = s * b0;
-                    s1[i & 1] = GATED ? s * b1 : s0[i & 1];
+                    if (i + DEPTH >= FM) {
+#pragma unroll
+                        for (int q = 0; q < kLoads / 2 / DEPTH; ++q) load_part(t + 2, (i + DEPTH - FM) * (kLoads / 2 / DEPTH) + q, off2);
+                    }
+                    const float t0 = s0, t1 = s1;
+                    s0 = sa[i >> 2][i & 3] * b0;
+                    s1 = GATED ? sa[i >> 2][i & 3] * b1 : s0;
+                    if (T::H > 1 && i + 1 < T::H) read_sa(i + 1);
+                    if (i + 1 == FM) {
+                        scales_of(t + 1);
+                        read_sa(0);
+                        read_b(t + 1);
+                    }
+                    const int f = (i + DEPTH) % FM;
+                    x[(i + DEPTH) % RING] = read(xa + (i + DEPTH < FM ? stage : next) + f * 2048);
 #pragma unroll
                     for (int j = 0; j < FN; ++j) {
-                        part[i & 1][j] = mma_block(w[j], x[i & 1]);
+                        part[i & 1][j] = mma_block(w[j], x[i % RING]);
                         if (i + 1 == FM) w[j] = read(wb + next + j * 2048);
                     }
-                    add((i + FM - 1) % FM);
-                    if (i + 1 == FM) {
-                        sc = scale_at(t + 1);
-                        sa = sc[srow];
-                        b0 = sc[sb0];
-                        b1 = sc[sb1];
-                    }
-                    // an MFMA, then what the vector ALU and LDS do beside it
+                    // meanwhile the last group's into their sums
+                    const int l = (i + FM - 1) % FM;
+#pragma unroll
+                    for (int j = 0; j < FN; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[j][l][e] = fmaf(part[l & 1][j][e], e & 1 ? t1 : t0, acc[j][l][e]);
+                    // an MFMA, then what the vector ALU, LDS and the loads do beside it
 #pragma unroll
                     for (int j = 0; j < FN; ++j) {
                         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                        if ((i < FM / 4 || i + DEPTH >= FM) && j % 2 == 0) __builtin_amdgcn_sched_group_barrier(0x020, kLoads / 8, 0);
                         if (i + 1 == FM) __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
                         else __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
                         __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);
@@ -195,7 +239,10 @@ __global__ __launch_bounds__(T::NT, 2) void gemm_blocks_kernel(const GemmBlocksA
                 }
             }
         }
-        add(FM - 1);
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[j][FM - 1][e] = fmaf(part[(FM - 1) & 1][j][e], e & 1 ? s1 : s0, acc[j][FM - 1][e]);
     }
 
     // ---- epilogue: lane holds row m0 + 16 (wm FM + i) + lane % 16, columns n0 + 16 (wn FN + j) + 4 (lane / 16) + e.
@@ -204,6 +251,22 @@ __global__ __launch_bounds__(T::NT, 2) void gemm_blocks_kernel(const GemmBlocksA
     constexpr int kMix = (kChunks < 16 ? kChunks : 16) - 1;      // chunk c of row r lies at c ^ (r & kMix)
     wait_vmcnt<0>();
     __syncthreads();
+    // the residual comes by loads of whole lines to where the outputs will lie
+    const bool staged = !GATED && p.residual && (p.n & 7) == 0;
+    if (staged) {
+        constexpr int kRows = 1024 / kRow;                       // of a load
+#pragma unroll
+        for (int l = 0; l < T::BM / kRows / T::NW; ++l) {
+            const int r0 = kRows * T::NW * l, r = kRows * wave + lane / kChunks, c = (lane % kChunks) ^ ((r0 + r) & kMix);
+            int64_t left = p.m - m0 - r0;
+            left = left < 0 ? 0 : left > kRows * T::NW ? kRows * T::NW : left;
+            const __amdgpu_buffer_rsrc_t rr = buffer_rsrc(p.residual + (m0 + r0) * p.n, static_cast<uint32_t>(left * p.n * 2));
+            load_lds16_buf(rr, n0 + 8 * c < p.n ? 2u * (static_cast<uint32_t>(r) * static_cast<uint32_t>(p.n) + n0 + 8 * c) : kOutOfRange,
+                           lds + (r0 + kRows * wave) * kRow);
+        }
+        wait_vmcnt<0>();
+        __syncthreads();
+    }
     const int64_t m_last = p.m - 1;
 #pragma unroll
     for (int j = 0; j < FN; ++j) {
@@ -216,29 +279,26 @@ __global__ __launch_bounds__(T::NT, 2) void gemm_blocks_kernel(const GemmBlocksA
 #pragma unroll
         for (int i = 0; i < FM; ++i) {
             const int ml = 16 * (wm * FM + i) + row;
+            const int at = GATED ? nl : 2 * nl;                  // bytes: columns nl / 2 and nl / 2 + 1, or the four
+            uint8_t* const to = lds + ml * kRow + (((at >> 4) ^ (ml & kMix)) << 4) + (at & 15);
             float v[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = acc[j][i][e] + sh[e];
             if constexpr (GATED) {
-                const int at = nl;          // bytes: columns nl / 2 and nl / 2 + 1
-                *reinterpret_cast<uint32_t*>(lds + ml * kRow + (((at >> 4) ^ (ml & kMix)) << 4) + (at & 15)) =
-                    pack_bf16x2(gate_act<ACT>(v[0]) * v[1], gate_act<ACT>(v[2]) * v[3]);
+                *reinterpret_cast<uint32_t*>(to) = pack_bf16x2(gate_act<ACT>(v[0]) * v[1], gate_act<ACT>(v[2]) * v[3]);
             } else {
-                if (p.residual) {
+                if (staged) {
+                    const uint2 r = *reinterpret_cast<const uint2*>(to);
+                    v[0] += __uint_as_float(r.x << 16);
+                    v[1] += __uint_as_float(r.x & 0xFFFF0000u);
+                    v[2] += __uint_as_float(r.y << 16);
+                    v[3] += __uint_as_float(r.y & 0xFFFF0000u);
+                } else if (p.residual) {
                     const int64_t mc = m0 + ml < m_last ? m0 + ml : m_last;
-                    if ((p.n & 3) == 0) {
-                        const uint2 r = *reinterpret_cast<const uint2*>(p.residual + mc * p.n + (n + 4 <= p.n ? n : p.n - 4));
-                        v[0] += __uint_as_float(r.x << 16);
-                        v[1] += __uint_as_float(r.x & 0xFFFF0000u);
-                        v[2] += __uint_as_float(r.y << 16);
-                        v[3] += __uint_as_float(r.y & 0xFFFF0000u);
-                    } else {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) v[e] += bf16_to_f32(p.residual[mc * p.n + (n + e < p.n ? n + e : p.n - 1)]);
-                    }
+                    for (int e = 0; e < 4; ++e) v[e] += bf16_to_f32(p.residual[mc * p.n + (n + e < p.n ? n + e : p.n - 1)]);
                 }
-                const int at = 2 * nl;
-                *reinterpret_cast<uint2*>(lds + ml * kRow + (((at >> 4) ^ (ml & kMix)) << 4) + (at & 15)) =
+                *reinterpret_cast<uint2*>(to) =
                     make_uint2(pack_bf16x2(activate<ACT>(v[0]), activate<ACT>(v[1])), pack_bf16x2(activate<ACT>(v[2]), activate<ACT>(v[3])));
             }
         }
@@ -263,7 +323,6 @@ __global__ __launch_bounds__(T::NT, 2) void gemm_blocks_kernel(const GemmBlocksA
 
 using Tile256 = BlockTile<2, 4, 8, 4>;      // 256 x 256, a wave 128 x 64
 using Tile128 = BlockTile<2, 2, 4, 4>;      // 128 x 128, a wave 64 x 64
-using Tile64 = BlockTile<2, 2, 2, 2>;       // 64 x 64, a wave 32 x 32
 
 template <class T, int ACT>
 hipError_t launch_tile(const GemmBlocksArgs& a, hipStream_t s) {
@@ -276,8 +335,7 @@ hipError_t launch_tile(const GemmBlocksArgs& a, hipStream_t s) {
 template <int ACT>
 hipError_t launch(const GemmBlocksArgs& a, hipStream_t s) {
     if (a.m > 512) return launch_tile<Tile256, ACT>(a, s);
-    if (a.m > 64) return launch_tile<Tile128, ACT>(a, s);
-    return launch_tile<Tile64, ACT>(a, s);
+    return launch_tile<Tile128, ACT>(a, s);
 }
 
 }  // namespace
