@@ -158,7 +158,8 @@ extern "C" dlf_status dlf_quant_blocks(const dlf_quant_blocks_desc* d, const voi
 
 namespace {
 
-dlf_status check_gemm_desc(const dlf_gemm_blocks_desc* d) {
+// the descriptor's checks; fills the kernels' sizes and their plan
+dlf_status check_gemm_desc(const dlf_gemm_blocks_desc* d, dlf::GemmBlocksArgs* g) {
     if (!d) return fail(DLF_ERR_INVALID_ARG, "gemm descriptor is NULL");
     if (d->act < DLF_ACT_NONE || d->act > DLF_ACT_GELU_ERF)
         return fail(DLF_ERR_INVALID_ARG, "unknown activation %d", static_cast<int>(d->act));
@@ -167,11 +168,23 @@ dlf_status check_gemm_desc(const dlf_gemm_blocks_desc* d) {
     if (d->n > kMaxCols || d->k > kMaxCols || d->m > (int64_t(1) << 24) || d->m * d->n >= (int64_t(1) << 38))
         return fail(DLF_ERR_UNSUPPORTED, "n and k must be at most 2^23, m at most 2^24, m * n below 2^38");
     dlf_status st = check_scale_stride(d->a_scale_stride, d->k);
-    return st != DLF_OK ? st : check_scale_stride(d->b_scale_stride, d->k);
+    if (st != DLF_OK || (st = check_scale_stride(d->b_scale_stride, d->k)) != DLF_OK) return st;
+    *g = dlf::GemmBlocksArgs{};
+    g->m = d->m;
+    g->n = d->n;
+    g->k = d->k;
+    g->a_scale_stride = d->a_scale_stride;
+    g->b_scale_stride = d->b_scale_stride;
+    dlf::plan_gemm_blocks(g);
+    return ok();
+}
+
+size_t gemm_ws_bytes(const dlf::GemmBlocksArgs& g) {
+    return g.parts > 1 ? static_cast<size_t>(g.parts) * static_cast<size_t>(g.m) * static_cast<size_t>(g.part_stride) * 4 : 0;
 }
 
 // both products; act as launch_gemm_blocks takes it
-dlf_status run_gemm(const dlf_gemm_blocks_desc* d, const void* a, const float* a_scale, const void* b, const float* b_scale,
+dlf_status run_gemm(const dlf_gemm_blocks_desc* d, dlf::GemmBlocksArgs& g, const void* a, const float* a_scale, const void* b, const float* b_scale,
                     const float* shift, const void* residual, int act, void* c, void* workspace, size_t workspace_bytes,
                     void* stream, const char* what) {
     if (d->m == 0 || d->n == 0) return ok();
@@ -182,9 +195,7 @@ dlf_status run_gemm(const dlf_gemm_blocks_desc* d, const void* a, const float* a
                           static_cast<const void*>(shift), residual, static_cast<const void*>(c),
                           static_cast<const void*>(workspace)})
         if (!aligned(p, 16)) return fail(DLF_ERR_INVALID_ARG, "device pointers must be 16-byte aligned");
-    size_t need = 0;
-    const dlf_status st = dlf_gemm_blocks_workspace_bytes(d, &need);
-    if (st != DLF_OK) return st;
+    const size_t need = gemm_ws_bytes(g);
     if (need > 0 && (!workspace || workspace_bytes < need))
         return fail(DLF_ERR_INVALID_ARG, "workspace of %zu bytes needed (dlf_gemm_blocks_workspace_bytes), got %zu", need,
                     workspace ? workspace_bytes : size_t(0));
@@ -195,7 +206,6 @@ dlf_status run_gemm(const dlf_gemm_blocks_desc* d, const void* a, const float* a
                                {b_scale, rows_bytes(slabs, d->b_scale_stride, d->b_scale_stride, 4)}, {shift, n * 4},
                                {residual, m * n * 2}}))
         return fail(DLF_ERR_ALIAS, "the output or the workspace overlaps an operand");
-    dlf::GemmBlocksArgs g{};
     g.a = static_cast<const uint8_t*>(a);
     g.a_scale = a_scale;
     g.b = static_cast<const uint8_t*>(b);
@@ -203,11 +213,7 @@ dlf_status run_gemm(const dlf_gemm_blocks_desc* d, const void* a, const float* a
     g.shift = shift;
     g.residual = static_cast<const uint16_t*>(residual);
     g.c = static_cast<uint16_t*>(c);
-    g.m = d->m;
-    g.n = d->n;
-    g.k = d->k;
-    g.a_scale_stride = d->a_scale_stride;
-    g.b_scale_stride = d->b_scale_stride;
+    g.part = static_cast<float*>(workspace);
     return hip_status(dlf::launch_gemm_blocks(g, act, static_cast<hipStream_t>(stream)), what);
 }
 
@@ -216,30 +222,35 @@ dlf_status run_gemm(const dlf_gemm_blocks_desc* d, const void* a, const float* a
 extern "C" dlf_status dlf_gemm_blocks_workspace_bytes(const dlf_gemm_blocks_desc* d, size_t* bytes) {
     if (!bytes) return fail(DLF_ERR_INVALID_ARG, "bytes is NULL");
     *bytes = 0;
-    return check_gemm_desc(d);
+    dlf::GemmBlocksArgs g;
+    const dlf_status st = check_gemm_desc(d, &g);
+    if (st == DLF_OK && d->m > 0 && d->n > 0) *bytes = gemm_ws_bytes(g);
+    return st;
 }
 
 extern "C" dlf_status dlf_gemm_blocks(const dlf_gemm_blocks_desc* d, const void* a, const float* a_scale, const void* b,
                                       const float* b_scale, const float* col_shift, const void* residual, void* c,
                                       void* workspace, size_t workspace_bytes, void* stream) {
-    const dlf_status st = check_gemm_desc(d);
+    dlf::GemmBlocksArgs g;
+    const dlf_status st = check_gemm_desc(d, &g);
     if (st != DLF_OK) return st;
     const int act = d->act == DLF_ACT_RELU ? dlf::kActRelu : d->act == DLF_ACT_GELU_TANH ? dlf::kActGelu
                     : d->act == DLF_ACT_GELU_ERF ? dlf::kActGeluErf : dlf::kActNone;
-    return run_gemm(d, a, a_scale, b, b_scale, col_shift, residual, act, c, workspace, workspace_bytes, stream, "dlf_gemm_blocks");
+    return run_gemm(d, g, a, a_scale, b, b_scale, col_shift, residual, act, c, workspace, workspace_bytes, stream, "dlf_gemm_blocks");
 }
 
 extern "C" dlf_status dlf_gemm_blocks_gated(const dlf_gemm_blocks_desc* d, const void* a, const float* a_scale, const void* b,
                                             const float* b_scale, const float* col_shift, dlf_gate gate, void* c,
                                             void* workspace, size_t workspace_bytes, void* stream) {
-    const dlf_status st = check_gemm_desc(d);
+    dlf::GemmBlocksArgs g;
+    const dlf_status st = check_gemm_desc(d, &g);
     if (st != DLF_OK) return st;
     if (gate < DLF_GATE_SILU || gate > DLF_GATE_GELU_ERF)
         return fail(DLF_ERR_INVALID_ARG, "unknown gate %d", static_cast<int>(gate));
     if (d->act != DLF_ACT_NONE) return fail(DLF_ERR_INVALID_ARG, "the gate is the activation: act must be NONE");
     if (d->n % 2 != 0) return fail(DLF_ERR_INVALID_ARG, "n counts gate and up rows: it must be even");
     const int act = gate == DLF_GATE_SILU ? dlf::kActSiluMul : gate == DLF_GATE_GELU_TANH ? dlf::kActGeluMul : dlf::kActGeluErfMul;
-    return run_gemm(d, a, a_scale, b, b_scale, col_shift, nullptr, act, c, workspace, workspace_bytes, stream,
+    return run_gemm(d, g, a, a_scale, b, b_scale, col_shift, nullptr, act, c, workspace, workspace_bytes, stream,
                     "dlf_gemm_blocks_gated");
 }
 

@@ -1,24 +1,13 @@
-// Product of e4m3 matrices with block scales:
-//     acc[i][j] = sum_t a_scale[i][t] b_scale[j / 128][t] sum_{k in t} a[i][k] b[j][k],   t = blocks of 128 of k
-//     c = act(acc + shift [+ residual]),  or gate(acc[2j]) * acc[2j + 1]
-//
-// v_mfma_f32_16x16x128_f8f6f4 sums just one block: its result, from a zero start, is scaled and added to
-// the fp32 sum by one FMA a value.
-#include "block_scale.h"
-#include "kernels.h"
-#include "mma_common.h"
+// Products with block scales: tiles of 64 x 64 to 256 x 256 outputs a workgroup, and the choice among the kernels.
+#include "gemm_blocks.h"
 
 namespace dlf {
 namespace {
 
-// the unscaled form, both operands e4m3
-__device__ __forceinline__ f32x4_t mma_block(const i32x8_t& a, const i32x8_t& b) {
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, f32x4_t{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0, 0, 0);
-}
-
 // A workgroup's tile: WM x WN waves, each of FM x FN fragments of 16 rows of a and 16 of b.
-template <int WM_, int WN_, int FM_, int FN_>
+template <int WM_, int WN_, int FM_, int FN_, int WAVES_ = 2>
 struct BlockTile {
+    static constexpr int kWaves = WAVES_;                       // on a SIMD at least: its registers are shared by that many
     static constexpr int WM = WM_, WN = WN_, FM = FM_, FN = FN_;
     static constexpr int BM = 16 * WM * FM, BN = 16 * WN * FN;
     static constexpr int NW = WM * WN, NT = 64 * NW;
@@ -32,7 +21,7 @@ struct BlockTile {
     static constexpr int kScales = (kGroup * kARow + 2 * kGroup) * 4;
     static constexpr int kOut = BM * BN * 2;                    // the staged output
     static constexpr int kLds = 2 * kStage + 2 * kScales > kOut ? 2 * kStage + 2 * kScales : kOut;
-    static_assert(FM % 4 == 0 && (LA + LB) % 8 == 0, "fragments and loads in turn");
+    static_assert(FM % 4 == 0 && (LA + LB) % 4 == 0, "fragments and loads in turn");
     static_assert(LA >= 1 && LB >= 1 && BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && NW % 2 == 0, "whole loads");
     static_assert(BM % 64 == 0 && (BN == 128 || BN == 256 || BN == 64), "scales of whole waves, at most two rows of b's");
 };
@@ -50,7 +39,7 @@ __device__ __forceinline__ void xcd_tile(int tiles_m, int tiles_n, int bid, int&
 }
 
 template <class T, int ACT>
-__global__ __launch_bounds__(T::NT, 2) void gemm_blocks_kernel(const GemmBlocksArgs p, const int tiles_m, const int tiles_n) {
+__global__ __launch_bounds__(T::NT, T::kWaves) void gemm_blocks_kernel(const GemmBlocksArgs p, const int tiles_m, const int tiles_n) {
     constexpr bool GATED = ACT >= kActSiluMul;
     constexpr int FM = T::FM, FN = T::FN;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[T::kLds];
@@ -61,7 +50,10 @@ __global__ __launch_bounds__(T::NT, 2) void gemm_blocks_kernel(const GemmBlocksA
     xcd_tile<8>(tiles_m, tiles_n, static_cast<int>(blockIdx.x), tm, tn);
     const int64_t m0 = static_cast<int64_t>(tm) * T::BM;
     const int n0 = tn * T::BN;
-    const int k = p.k, blocks = (k + kScaleBlock - 1) / kScaleBlock;
+    const int k = p.k;
+    // this part's blocks of k: `blocks` from `begin` on, a multiple of 4
+    const int begin = static_cast<int>(blockIdx.y) * p.part_blocks, all = (k + kScaleBlock - 1) / kScaleBlock;
+    const int blocks = begin + p.part_blocks < all ? p.part_blocks : all - begin;
     const int g = lane >> 4, row = lane & 15;
 
     // Loads: 8 rows of 128 bytes an instruction, whole lines.  Load j of a wave takes rows 8 (wave + NW j) + lane / 8;
@@ -91,7 +83,7 @@ __global__ __launch_bounds__(T::NT, 2) void gemm_blocks_kernel(const GemmBlocksA
     constexpr int kLoads = T::LA + T::LB;
     // load q of this wave's of block t, whose offset is `off`; past the last block and past k: zeros
     auto load_off = [&](int t) {
-        const uint32_t at = static_cast<uint32_t>(t) * kScaleBlock;
+        const uint32_t at = static_cast<uint32_t>(begin + t) * kScaleBlock;
         return static_cast<int>(at) + 16 * chunk < k ? from + at : kOutOfRange;
     };
     auto load_part = [&](int t, int q, uint32_t off) {
@@ -107,7 +99,7 @@ __global__ __launch_bounds__(T::NT, 2) void gemm_blocks_kernel(const GemmBlocksA
     u32x4_t next_a{0u, 0u, 0u, 0u};
     uint32_t next_b = 0;
     auto fetch_scales = [&](int u) {
-        const uint32_t at = static_cast<uint32_t>(u) * (T::kGroup * 4);
+        const uint32_t at = static_cast<uint32_t>(begin + u * T::kGroup) * 4u;
         next_a = __builtin_amdgcn_raw_buffer_load_b128(
             rsa, mine ? static_cast<uint32_t>(arow) * static_cast<uint32_t>(p.a_scale_stride) * 4u + at + 16u * (lane & 1) : kOutOfRange, 0, 0);
         if (wave == 0)
@@ -230,7 +222,7 @@ __global__ __launch_bounds__(T::NT, 2) void gemm_blocks_kernel(const GemmBlocksA
 #pragma unroll
                     for (int j = 0; j < FN; ++j) {
                         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                        if ((i < FM / 4 || i + DEPTH >= FM) && j % 2 == 0) __builtin_amdgcn_sched_group_barrier(0x020, kLoads / 8, 0);
+                        if ((i < FM / 4 || i + DEPTH >= FM) && j % 2 == 0) __builtin_amdgcn_sched_group_barrier(0x020, kLoads >= 8 ? kLoads / 8 : 1, 0);
                         if (i + 1 == FM) __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
                         else __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
                         __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);
@@ -245,6 +237,19 @@ __global__ __launch_bounds__(T::NT, 2) void gemm_blocks_kernel(const GemmBlocksA
             for (int e = 0; e < 4; ++e) acc[j][FM - 1][e] = fmaf(part[(FM - 1) & 1][j][e], e & 1 ? s1 : s0, acc[j][FM - 1][e]);
     }
 
+    // a part of the sum goes to the workspace as it is
+    if (p.parts > 1) {
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int i = 0; i < FM; ++i) {
+                const int64_t m = m0 + 16 * (wm * FM + i) + row;
+                const int n = n0 + 16 * (wn * FN + j) + 4 * g;
+                if (m >= p.m || n >= p.part_stride) continue;
+                *reinterpret_cast<f32x4_t*>(p.part + (blockIdx.y * p.m + m) * p.part_stride + n) = acc[j][i];
+            }
+        return;
+    }
     // ---- epilogue: lane holds row m0 + 16 (wm FM + i) + lane % 16, columns n0 + 16 (wn FN + j) + 4 (lane / 16) + e.
     // The rounded tile goes through LDS, so that every output is written by a 16-byte store of whole lines. ----
     constexpr int kRow = (GATED ? T::BN / 2 : T::BN) * 2, kChunks = kRow / 16;
@@ -323,33 +328,108 @@ __global__ __launch_bounds__(T::NT, 2) void gemm_blocks_kernel(const GemmBlocksA
 
 using Tile256 = BlockTile<2, 4, 8, 4>;      // 256 x 256, a wave 128 x 64
 using Tile128 = BlockTile<2, 2, 4, 4>;      // 128 x 128, a wave 64 x 64
+using Tile64 = BlockTile<1, 4, 4, 1, 4>;    // 64 x 64, a wave 64 x 16
 
 template <class T, int ACT>
 hipError_t launch_tile(const GemmBlocksArgs& a, hipStream_t s) {
     const int64_t tiles_m = (a.m + T::BM - 1) / T::BM, tiles_n = (a.n + T::BN - 1) / T::BN;
     if (tiles_m * tiles_n >= kMaxWorkgroups / 2) return hipErrorInvalidValue;
-    gemm_blocks_kernel<T, ACT><<<static_cast<unsigned>(tiles_m * tiles_n), T::NT, 0, s>>>(a, static_cast<int>(tiles_m), static_cast<int>(tiles_n));
+    const dim3 grid(static_cast<unsigned>(tiles_m * tiles_n), static_cast<unsigned>(a.parts));
+    gemm_blocks_kernel<T, ACT><<<grid, T::NT, 0, s>>>(a, static_cast<int>(tiles_m), static_cast<int>(tiles_n));
     return hipGetLastError();
 }
 
 template <int ACT>
 hipError_t launch(const GemmBlocksArgs& a, hipStream_t s) {
-    if (a.m > 512) return launch_tile<Tile256, ACT>(a, s);
-    return launch_tile<Tile128, ACT>(a, s);
+    switch (a.kind) {
+        case kGemmBlocksTile64: return launch_tile<Tile64, ACT>(a, s);
+        case kGemmBlocksTile128: return launch_tile<Tile128, ACT>(a, s);
+        default: return launch_tile<Tile256, ACT>(a, s);
+    }
 }
+
+// A workgroup that shares a CU with w - 1 others takes slope + share w us a block of k and `more` us besides (measured over 180
+// sizes, 48 to 8192 rows; on average the choice below is 1% slower than the best of all).
+struct TileCost {
+    int kind, rows, cols, on_a_cu;
+    double slope, share, more;
+};
+constexpr TileCost kCosts[] = {
+    {kGemmBlocksTile64, 64, 64, 4, 0.31, 0.127, 0.2},
+    {kGemmBlocksTile128, 128, 128, 2, 0.40, 0.29, 1.0},
+    {kGemmBlocksTile256, 256, 256, 1, 0.0, 1.25, 4.0},
+};
 
 }  // namespace
 
-hipError_t launch_gemm_blocks(const GemmBlocksArgs& a, int act, hipStream_t s) {
-    switch (act) {
-        case kActNone: return launch<kActNone>(a, s);
-        case kActRelu: return launch<kActRelu>(a, s);
-        case kActGelu: return launch<kActGelu>(a, s);
-        case kActGeluErf: return launch<kActGeluErf>(a, s);
-        case kActSiluMul: return launch<kActSiluMul>(a, s);
-        case kActGeluMul: return launch<kActGeluMul>(a, s);
-        default: return launch<kActGeluErfMul>(a, s);
+// Up to 32 rows: the kernel for few rows.  32 rows of b a workgroup instead of 16 from 6144 columns on (us, 16 | 32, one
+// row of 4096: 4096 columns 6.1 | 6.2, 8192 9.4 | 8.4, 22016 22 | 18.5).  A sum of more than 8 turns a wave
+// is cut into parts where the columns alone leave CUs idle (one row of 11008, 1024 columns: 7.2 | 6.5 in 4 parts; 2048
+// columns of 4096 stay whole: 4.6 | 5.9).
+// Above: the tile and the parts of the sum that the costs above say.  Parts are joined by another launch and 8 bytes an output
+// and part.
+void plan_gemm_blocks(GemmBlocksArgs* a) {
+    constexpr int kCus = 256;
+    const int all = (a->k + kScaleBlock - 1) / kScaleBlock;
+    a->parts = 1;
+    a->part_blocks = all;
+    a->part_stride = (a->n + 3) / 4 * 4;
+    a->kind = kGemmBlocks16;
+    if (a->m == 0 || a->n == 0) return;
+    // whole fours of blocks a part: their scales are one load
+    auto cut = [&](int want, int* blocks) {
+        if (want == 1 || all == 0) {
+            *blocks = all;
+            return 1;
+        }
+        *blocks = ((all + want - 1) / want + 3) / 4 * 4;
+        return (all + *blocks - 1) / *blocks;
+    };
+    if (a->m <= 32) {
+        const bool wide = a->n > 6144;
+        a->kind = a->m <= 16 ? (wide ? kGemmBlocks16Wide : kGemmBlocks16) : (wide ? kGemmBlocks32Wide : kGemmBlocks32);
+        const int groups = (a->n + 15) / 16;
+        if (all > 32 && !wide && groups <= kCus / 2) {
+            const int want = kCus / groups;
+            a->parts = cut(want < 8 ? want : 8, &a->part_blocks);
+        }
+        return;
     }
+    double best = 0;
+    for (const TileCost& c : kCosts) {
+        const int64_t tiles = (a->m + c.rows - 1) / c.rows * ((a->n + c.cols - 1) / c.cols);
+        for (int want : {1, 2, 3, 4, 6, 8}) {
+            int blocks;
+            const int parts = cut(want, &blocks);
+            if (parts != want || (parts > 1 && tiles >= 4 * kCus)) continue;
+            const int64_t groups = tiles * parts, full = groups / (kCus * c.on_a_cu), rest = groups - full * kCus * c.on_a_cu;
+            double us = static_cast<double>(full) * (blocks * (c.slope + c.share * c.on_a_cu) + c.more);
+            if (rest > 0) us += blocks * (c.slope + c.share * static_cast<double>((rest + kCus - 1) / kCus)) + c.more;
+            if (parts > 1) us += 2.0 + parts * static_cast<double>(a->m) * a->n * 8 / 5.6e6;
+            if (best == 0 || us < best) {
+                best = us;
+                a->kind = c.kind;
+                a->parts = parts;
+                a->part_blocks = blocks;
+            }
+        }
+    }
+}
+
+hipError_t launch_gemm_blocks(const GemmBlocksArgs& a, int act, hipStream_t s) {
+    auto go = [&]() -> hipError_t {
+        switch (act) {
+            case kActNone: return launch<kActNone>(a, s);
+            case kActRelu: return launch<kActRelu>(a, s);
+            case kActGelu: return launch<kActGelu>(a, s);
+            case kActGeluErf: return launch<kActGeluErf>(a, s);
+            case kActSiluMul: return launch<kActSiluMul>(a, s);
+            case kActGeluMul: return launch<kActGeluMul>(a, s);
+            default: return launch<kActGeluErfMul>(a, s);
+        }
+    };
+    const hipError_t e = a.kind <= kGemmBlocks32Wide ? launch_gemm_blocks_skinny(a, act, s) : go();
+    return e != hipSuccess || a.parts == 1 ? e : launch_gemm_blocks_join(a, act, s);
 }
 
 }  // namespace dlf

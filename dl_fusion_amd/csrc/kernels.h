@@ -281,8 +281,21 @@ struct GemmBlocksArgs {
     int64_t m;
     int n, k;
     int a_scale_stride, b_scale_stride;
+    int kind;                   // kGemmBlocks*
+    // the sum over k in parts (> 1: each goes to the workspace, and a second kernel joins them)
+    int parts, part_blocks;     // part_blocks: blocks of 128 of a part, a multiple of 4 where there are several
+    int part_stride;            // n, rounded up to a multiple of 4
+    float* part;                // [parts][m][part_stride]
 };
+// the kernels: up to 16 or 32 rows of a, 16 rows of b a workgroup or 32, and tiles
+enum : int {
+    kGemmBlocks16 = 0, kGemmBlocks16Wide = 1, kGemmBlocks32 = 2, kGemmBlocks32Wide = 3,
+    kGemmBlocksTile64 = 4, kGemmBlocksTile128 = 5, kGemmBlocksTile256 = 6
+};
+void plan_gemm_blocks(GemmBlocksArgs* args);    // fills kind, parts, part_blocks and part_stride from m, n and k
 // act: kAct*, or kActSiluMul.. for the gated form
+hipError_t launch_gemm_blocks_skinny(const GemmBlocksArgs& args, int act, hipStream_t stream);
+hipError_t launch_gemm_blocks_join(const GemmBlocksArgs& args, int act, hipStream_t stream);
 hipError_t launch_gemm_blocks(const GemmBlocksArgs& args, int act, hipStream_t stream);
 
 // Shader-clock probe: workgroups x 4 waves of back-to-back bf16 MFMAs; stamps[4 b + 0..3] =

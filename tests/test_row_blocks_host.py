@@ -191,6 +191,31 @@ def test_product_refusals():
     assert call_gemm(gate=0, act="relu") == INVALID
 
 
+@pytest.mark.parametrize("m", [0, 1, 16, 17, 32, 33, 64, 65, 200, 777, 4096, 1 << 24])
+def test_workspace_sizes(m):
+    """Whole fp32 outputs, rows rounded up to 4 columns, at most 8 of them; none where nothing is summed."""
+    for n in (0, 1, 2, 5, 64, 300, 1024, 4096, 22016):
+        for k in (0, 16, 128, 1024, 4096, 11008, 1 << 23):
+            if m * n >= 1 << 38:
+                continue
+            size = dlf.dlf_gemm_blocks_workspace_bytes(dlf.gemm_blocks_desc(m, n, k))
+            one = m * (-(-n // 4) * 4) * 4
+            assert size == 0 if one == 0 else size % one == 0 and size // one <= 8 and size // one != 1
+            assert size == 0 or k > 128
+    assert dlf.dlf_gemm_blocks_workspace_bytes(dlf.gemm_blocks_desc(64, 4096, 11008)) > 0
+    assert dlf.dlf_gemm_blocks_workspace_bytes(dlf.gemm_blocks_desc(1, 4096, 4096)) == 0
+
+
+@fake_pointers
+def test_product_refuses_a_bad_workspace():
+    size = dlf.dlf_gemm_blocks_workspace_bytes(dlf.gemm_blocks_desc(64, 4096, 11008))
+    big = dict(m=64, n=4096, k=11008)
+    assert call_gemm(workspace=None, **big) == INVALID and call_gemm(workspace_bytes=size - 1, **big) == INVALID
+    assert call_gemm(gate=0, workspace=None, **big) == INVALID
+    for i in (0, 1, 2, 3, 4, 5, 6):
+        assert call_gemm(workspace=addr(i, 256), **big) == ALIAS, i
+
+
 def test_product_binding_checks_tensors():
     m, n, k = 4, 256, 512
     d = dlf.gemm_blocks_desc(m, n, k)
