@@ -257,6 +257,7 @@ struct RmsNormArgs {
 };
 // out: kOutBf16 / kOutF32 / kOutFp8 (block scales where scale is given, else inv_scale)
 hipError_t launch_rms_norm(const RmsNormArgs& args, bool f32, int out, hipStream_t stream);
+hipError_t launch_rms_norm_f32(const RmsNormArgs& args, int out, hipStream_t stream);
 
 // Rows into e4m3 codes with a scale for each 128 columns (dlf_quant_blocks).
 struct QuantBlocksArgs {
@@ -268,6 +269,7 @@ struct QuantBlocksArgs {
     int cols, row_blocks, scale_stride;
 };
 hipError_t launch_quant_blocks(const QuantBlocksArgs& args, bool f32, hipStream_t stream);
+hipError_t launch_quant_blocks_f32(const QuantBlocksArgs& args, hipStream_t stream);
 
 // Product of e4m3 matrices with block scales (dlf_gemm_blocks, dlf_gemm_blocks_gated).
 struct GemmBlocksArgs {

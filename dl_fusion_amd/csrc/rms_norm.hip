@@ -1,276 +1,15 @@
-// Root-mean-square norm of rows with the residual's addition, and the quantiser of rows into e4m3 codes
-// with a scale for each 128 columns.
-//
-//     h = x [+ residual],  sum = h,  y = h / sqrt(mean(h^2) + eps) * weight
-//
-// Both read each value once and write each output once, and have nothing to compute beside: HBM bounds them,
-// or the launch where there are few rows.  A thread holds 8 neighbouring columns at a time, so that a row
-// is read in whole lines and 16 neighbouring lanes hold a block of 128 columns: its largest magnitude is a
-// maximum over those lanes, no LDS.
-#include "block_scale.h"
-#include "kernels.h"
+// The norm and the block quantiser of bf16 rows, and the choice between the types (rms_norm.h has the kernels,
+// rms_norm_f32.hip those of fp32 rows; two files, so that they compile at the same time).
+#include "rms_norm.h"
 
 namespace dlf {
-namespace {
-
-enum : int { kYBf16 = 0, kYF32 = 1, kYStatic = 2, kYBlocks = 3 };
-
-// 16 bytes at any address that the element type allows: rows of odd width or stride start anywhere, and the
-// hardware takes such loads.
-typedef u32x4_t u32x4_any_t __attribute__((aligned(2)));
-typedef f32x4_t f32x4_any_t __attribute__((aligned(4)));
-typedef uint32_t u32x2_any_t __attribute__((ext_vector_type(2), aligned(1)));
-
-__device__ __forceinline__ void load8(const uint16_t* p, float* v) {
-    const u32x4_t x = *reinterpret_cast<const u32x4_any_t*>(p);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(x[i] << 16);
-        v[2 * i + 1] = __uint_as_float(x[i] & 0xFFFF0000u);
-    }
-}
-__device__ __forceinline__ void load8(const float* p, float* v) {
-    const f32x4_t a = *reinterpret_cast<const f32x4_any_t*>(p), b = *reinterpret_cast<const f32x4_any_t*>(p + 4);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) { v[i] = a[i]; v[4 + i] = b[i]; }
-}
-__device__ __forceinline__ float load1(const uint16_t* p) { return bf16_to_f32(*p); }
-__device__ __forceinline__ float load1(const float* p) { return *p; }
-
-// n < 8 values of a row's end, zeros behind them
-template <typename T>
-__device__ __forceinline__ void load_chunk(const T* p, int n, float* v) {
-    if (n >= 8) {
-        load8(p, v);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = i < n ? load1(p + i) : 0.0f;
-    }
-}
-
-__device__ __forceinline__ void store_chunk(uint16_t* p, int n, const float* v) {
-    if (n >= 8) {
-        u32x4_t x;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-        *reinterpret_cast<u32x4_any_t*>(p) = x;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < n) p[i] = f32_to_bf16(v[i]);
-    }
-}
-__device__ __forceinline__ void store_chunk(float* p, int n, const float* v) {
-    if (n >= 8) {
-        *reinterpret_cast<f32x4_any_t*>(p) = f32x4_t{v[0], v[1], v[2], v[3]};
-        *reinterpret_cast<f32x4_any_t*>(p + 4) = f32x4_t{v[4], v[5], v[6], v[7]};
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < n) p[i] = v[i];
-    }
-}
-__device__ __forceinline__ void store_codes(uint8_t* p, int n, const float* v, float inv) {
-    const uint32_t lo = e4m3_x4(v, inv), hi = e4m3_x4(v + 4, inv);
-    if (n >= 8) {
-        *reinterpret_cast<u32x2_any_t*>(p) = u32x2_any_t{lo, hi};
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < n) p[i] = static_cast<uint8_t>((i < 4 ? lo : hi) >> (8 * (i & 3)));
-    }
-}
-
-// The block of the 16 lanes that hold 8 columns each: its scale, and the codes.  Lanes past the row's end
-// hold zeros.
-__device__ __forceinline__ void store_block(const float* v, int n, int lane, uint8_t* codes, float* scale) {
-    float top = kLeastMax;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) top = fmaxf(top, finite_abs(v[i]));
-#pragma unroll
-    for (int d = 8; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
-    if (n > 0) {
-        if ((lane & 15) == 0) *scale = top / 448.0f;
-        store_codes(codes, n, v, 448.0f / top);
-    }
-}
-
-// A row per group of TPR threads, V chunks of 8 columns a thread in registers; V = 0: rows beyond that, read
-// again from memory for the second pass.  Each element is read by the thread that writes it, and written after
-// both passes have read it or in place of it: sum and y may be an input itself.
-template <typename T, int OUT, int TPR, int V>
-__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rms_norm_kernel(const RmsNormArgs p) {
-    constexpr int kRows = TPR < 256 ? 256 / TPR : 1;
-    constexpr int kWaves = TPR / 64;
-    __shared__ float part[kWaves];
-    const int tid = static_cast<int>(threadIdx.x) % TPR, lane = tid & 63;
-    const int cols = p.cols;
-    const float* const w = p.weight;
-    // every thread of a workgroup takes as many turns: the barriers below are met by all
-    for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * kRows; row0 < p.rows; row0 += static_cast<int64_t>(gridDim.x) * kRows) {
-        const int64_t row = row0 + static_cast<int>(threadIdx.x) / TPR;
-        if (kRows > 1 && row >= p.rows) return;         // no barrier where rows share a workgroup
-        const T* const x = static_cast<const T*>(p.x) + row * p.x_stride;
-        const T* const res = p.residual ? static_cast<const T*>(p.residual) + row * p.residual_stride : nullptr;
-        T* const sum = p.sum ? static_cast<T*>(p.sum) + row * p.sum_stride : nullptr;
-        auto load_h = [&](int at, float* h) __attribute__((always_inline)) {
-            load_chunk(x + at, cols - at, h);
-            if (res) {
-                float r[8];
-                load_chunk(res + at, cols - at, r);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) h[i] += r[i];
-            }
-        };
-        auto all_sum = [&](float s) __attribute__((always_inline)) {
-#pragma unroll
-            for (int d = 32; d > 0; d >>= 1) s += __shfl_xor(s, d);
-            if constexpr (kWaves > 1) {
-                __syncthreads();                        // the last sum has been read
-                if (lane == 0) part[tid / 64] = s;
-                __syncthreads();
-                s = 0.0f;
-#pragma unroll
-                for (int i = 0; i < kWaves; ++i) s += part[i];
-            }
-            return s;
-        };
-        float h[V > 0 ? V : 1][8];
-        auto squares = [&](float factor) __attribute__((always_inline)) {
-            float s = 0.0f;
-            auto add = [&](const float* v) __attribute__((always_inline)) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float u = v[i] * factor;
-                    s = fmaf(u, u, s);
-                }
-            };
-            if constexpr (V > 0) {
-#pragma unroll
-                for (int j = 0; j < V; ++j) add(h[j]);
-            } else {
-                for (int at = 8 * tid; at < cols; at += 8 * TPR) {
-                    load_h(at, h[0]);
-                    add(h[0]);
-                }
-            }
-            return all_sum(s);
-        };
-        if constexpr (V > 0) {
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int at = 8 * (tid + j * TPR);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) h[j][i] = 0.0f;
-                if (at < cols) load_h(at, h[j]);
-            }
-        }
-        float total = squares(1.0f);
-        float factor = 1.0f, eps = p.eps;
-        if (__builtin_expect(total == INFINITY, 0)) {
-            // past fp32's range, or an infinity among them: the row 2^-80 times as large (2^23 squares of 2^48
-            // fit), where eps is nothing beside it; h * r itself would need an r below the normal numbers
-            factor = 0x1p-80f;
-            eps = 0.0f;
-            total = squares(factor);
-        }
-        const float r = 1.0f / sqrtf(total / static_cast<float>(cols) + eps);
-        auto finish = [&](int at, const float* v) __attribute__((always_inline)) {
-            const int n = cols - at;
-            float y[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = v[i] * factor * r;
-            if (w && n > 0) {
-                float f[8];
-                load_chunk(w + at, n, f);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] *= f[i];
-            }
-            if (sum && n > 0) store_chunk(sum + at, n, v);
-            if constexpr (OUT == kYBlocks) {
-                if (n < 8) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) y[i] = i < n ? y[i] : 0.0f;     // 0 x infinity past the end
-                }
-                store_block(y, n, lane, static_cast<uint8_t*>(p.y) + row * p.y_stride + at,
-                            p.scale + row * p.scale_stride + at / kScaleBlock);
-            } else if (n > 0) {
-                if constexpr (OUT == kYBf16) store_chunk(static_cast<uint16_t*>(p.y) + row * p.y_stride + at, n, y);
-                else if constexpr (OUT == kYF32) store_chunk(static_cast<float*>(p.y) + row * p.y_stride + at, n, y);
-                else store_codes(static_cast<uint8_t*>(p.y) + row * p.y_stride + at, n, y, p.inv_scale);
-            }
-        };
-        if constexpr (V > 0) {
-#pragma unroll
-            for (int j = 0; j < V; ++j) finish(8 * (tid + j * TPR), h[j]);
-        } else {
-            // all lanes of a block's 16 go together
-            for (int base = 0; base < cols; base += 8 * TPR) {
-                const int at = base + 8 * tid;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) h[0][i] = 0.0f;
-                if (at < cols) load_h(at, h[0]);
-                finish(at, h[0]);
-            }
-        }
-    }
-}
-
-// 16 lanes a block of 128 columns, blocks numbered row by row.
-template <typename T>
-__global__ __launch_bounds__(256) void quant_blocks_kernel(const QuantBlocksArgs p) {
-    for (uint32_t block = blockIdx.x * 16 + threadIdx.x / 16; block < p.blocks; block += gridDim.x * 16) {
-        const uint32_t row = block / static_cast<uint32_t>(p.row_blocks), b = block - row * static_cast<uint32_t>(p.row_blocks);
-        const int lane = static_cast<int>(threadIdx.x) & 15, at = static_cast<int>(b) * kScaleBlock + 8 * lane;
-        float v[8] = {};
-        if (at < p.cols) load_chunk(static_cast<const T*>(p.x) + row * p.x_stride + at, p.cols - at, v);
-        store_block(v, p.cols - at, lane, p.codes + row * p.codes_stride + at,
-                    p.scale + static_cast<int64_t>(row) * p.scale_stride + b);
-    }
-}
-
-constexpr unsigned kMostGroups = 1u << 20;      // workgroups of a launch; what is beyond comes round again
-
-template <typename T, int OUT>
-hipError_t launch(const RmsNormArgs& a, hipStream_t s) {
-    auto go = [&](auto kernel, int tpr) {
-        const int rows = tpr < 256 ? 256 / tpr : 1;
-        const int64_t groups = (a.rows + rows - 1) / rows;
-        kernel<<<groups < kMostGroups ? static_cast<unsigned>(groups) : kMostGroups, tpr < 256 ? 256 : tpr, 0, s>>>(a);
-        return hipGetLastError();
-    };
-    if (a.cols <= 512) return go(rms_norm_kernel<T, OUT, 64, 1>, 64);
-    if (a.cols <= 1024) return go(rms_norm_kernel<T, OUT, 64, 2>, 64);
-    if (a.cols <= 2048) return go(rms_norm_kernel<T, OUT, 256, 1>, 256);
-    if (a.cols <= 4096) return go(rms_norm_kernel<T, OUT, 256, 2>, 256);
-    if (a.cols <= 8192) return go(rms_norm_kernel<T, OUT, 512, 2>, 512);
-    if (a.cols <= 16384) return go(rms_norm_kernel<T, OUT, 1024, 2>, 1024);
-    return go(rms_norm_kernel<T, OUT, 1024, 0>, 1024);
-}
-
-template <typename T>
-hipError_t launch_out(const RmsNormArgs& a, int out, hipStream_t s) {
-    switch (out) {
-        case kYBf16: return launch<T, kYBf16>(a, s);
-        case kYF32: return launch<T, kYF32>(a, s);
-        case kYStatic: return launch<T, kYStatic>(a, s);
-        default: return launch<T, kYBlocks>(a, s);
-    }
-}
-
-}  // namespace
 
 hipError_t launch_rms_norm(const RmsNormArgs& a, bool f32, int out, hipStream_t s) {
-    if (out == kOutFp8 && a.scale) out = kYBlocks;
-    else out = out == kOutFp8 ? kYStatic : out == kOutF32 ? kYF32 : kYBf16;
-    return f32 ? launch_out<float>(a, out, s) : launch_out<uint16_t>(a, out, s);
+    return f32 ? launch_rms_norm_f32(a, out, s) : launch_out<uint16_t>(a, out, s);
 }
 
 hipError_t launch_quant_blocks(const QuantBlocksArgs& a, bool f32, hipStream_t s) {
-    const unsigned all = (a.blocks + 15) / 16, groups = all < kMostGroups ? all : kMostGroups;
-    if (f32) quant_blocks_kernel<float><<<groups, 256, 0, s>>>(a);
-    else quant_blocks_kernel<uint16_t><<<groups, 256, 0, s>>>(a);
-    return hipGetLastError();
+    return f32 ? launch_quant_blocks_f32(a, s) : launch_quant<uint16_t>(a, s);
 }
 
 }  // namespace dlf
