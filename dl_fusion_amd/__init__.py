@@ -569,48 +569,58 @@ def dlf_lora_add(desc, x, a, b, scale, ids, row_map, base, out, workspace, works
                              workspace_bytes, _stream(stream)), "dlf_lora_add")
 
 
-_TYPES = {DLF_F32: (_F32, 4), DLF_BF16: (_BF16, 2), DLF_FP8_E4M3: (_FP8, 1)}
+_TYPES = {DLF_F32: _F32, DLF_BF16: _BF16, DLF_FP8_E4M3: _FP8}
 
 
-def _strided(t, dtype, rows, cols, stride, name):
-    """Device pointer of a [rows][cols] tensor of the descriptor's type whose rows are `stride` elements apart,
-    or of a raw address or None as it is."""
-    if t is None or isinstance(t, int):
+def _strided(t, dtype, shape, stride, name):
+    """Device pointer of a tensor of the type and shape (rows, columns) that the descriptor says, its rows `stride`
+    elements apart, or of a raw address or None as it is.  0.4 us a tensor where it is just that."""
+    if t is None or t.__class__ is int:
         return t
-    want = _TYPES.get(dtype, (None, 0))[0]      # an unknown type is the library's to refuse
-    if want is not None and t.dtype is not want and t.dtype not in _BITS.get(want, ()):
-        raise ValueError(f"{name} has type {t.dtype}, {want} is needed")
-    shape, strides = t.shape, t.stride()
-    if len(shape) != 2 or shape[0] != rows or shape[1] != cols or (cols > 1 and strides[1] != 1) or (
-            rows > 1 and cols > 0 and strides[0] != stride):
-        raise ValueError(f"{name} must be [{rows}][{cols}] with rows {stride} elements apart")
+    if t.shape != shape or t.dtype is not dtype or not (t.is_contiguous() if stride == shape[1] else t.stride() == (stride, 1)):
+        _refuse_strided(t, dtype, shape, stride, name)
     return t.data_ptr()
+
+
+def _refuse_strided(t, dtype, shape, stride, name):
+    # an unknown type is the library's to refuse; the strides of a single row or column are not used
+    if dtype is not None and t.dtype is not dtype and t.dtype not in _BITS.get(dtype, ()):
+        raise ValueError(f"{name} has type {t.dtype}, {dtype} is needed")
+    rows, cols = shape
+    got = t.stride()
+    if tuple(t.shape) != shape or (cols > 1 and rows > 0 and got[1] != 1) or (rows > 1 and cols > 0 and got[0] != stride):
+        raise ValueError(f"{name} must be [{rows}][{cols}] with rows {stride} elements apart")
 
 
 def _scales(t, rows, stride, name):
     """Device pointer of contiguous fp32 block scales [rows][stride], or of a raw address or None as it is."""
-    return _sized(t, _F32, 4 * rows * stride, name)
+    if t is None or t.__class__ is int:
+        return t
+    if t.dtype is not _F32 or t.nbytes < 4 * rows * stride or not t.is_contiguous():
+        _refuse(t, _F32, 4 * rows * stride, name)
+    return t.data_ptr()
 
 
 def dlf_rms_norm(desc, x, residual, weight, sum, y, y_scale, stream=None):
     """y = norm(x + residual) * weight, and the sum itself (see include/dlfusion.h); the rows lie the descriptor's
     strides apart."""
-    n, cols, dtype = desc.rows, desc.cols, desc.dtype
-    _check(_lib.dlf_rms_norm(ctypes.byref(desc), _strided(x, dtype, n, cols, desc.x_stride, "x"),
-                             _strided(residual, dtype, n, cols, desc.residual_stride, "residual"),
-                             _sized(weight, _F32, 4 * cols, "weight"),
-                             _strided(sum, dtype, n, cols, desc.sum_stride, "sum"),
-                             _strided(y, desc.out_dtype, n, cols, desc.y_stride, "y"),
-                             _scales(y_scale, n, desc.scale_stride, "y_scale"), _stream(stream)),
-           "dlf_rms_norm")
+    n, cols = shape = desc.rows, desc.cols
+    dtype = _TYPES.get(desc.dtype)
+    _check(_lib.dlf_rms_norm(ctypes.byref(desc), _strided(x, dtype, shape, desc.x_stride, "x"),
+                             residual if residual is None else _strided(residual, dtype, shape, desc.residual_stride, "residual"),
+                             _scales(weight, 1, cols, "weight"),
+                             sum if sum is None else _strided(sum, dtype, shape, desc.sum_stride, "sum"),
+                             _strided(y, _TYPES.get(desc.out_dtype), shape, desc.y_stride, "y"),
+                             y_scale if y_scale is None else _scales(y_scale, n, desc.scale_stride, "y_scale"),
+                             _stream(stream)), "dlf_rms_norm")
 
 
 def dlf_quant_blocks(desc, x, codes, scale, stream=None):
     """Rows as e4m3 codes and a scale for each 128 columns (see include/dlfusion.h)."""
-    n, cols = desc.rows, desc.cols
-    _check(_lib.dlf_quant_blocks(ctypes.byref(desc), _strided(x, desc.dtype, n, cols, desc.x_stride, "x"),
-                                 _strided(codes, DLF_FP8_E4M3, n, cols, desc.codes_stride, "codes"),
-                                 _scales(scale, n, desc.scale_stride, "scale"), _stream(stream)),
+    shape = desc.rows, desc.cols
+    _check(_lib.dlf_quant_blocks(ctypes.byref(desc), _strided(x, _TYPES.get(desc.dtype), shape, desc.x_stride, "x"),
+                                 _strided(codes, _FP8, shape, desc.codes_stride, "codes"),
+                                 _scales(scale, shape[0], desc.scale_stride, "scale"), _stream(stream)),
            "dlf_quant_blocks")
 
 
@@ -620,33 +630,31 @@ def dlf_gemm_blocks_workspace_bytes(desc):
     return n.value
 
 
-def _gemm_blocks_operands(desc, a, a_scale, b, b_scale, col_shift, slabs):
-    m, n, k = desc.m, desc.n, desc.k
-    return (_strided(a, DLF_FP8_E4M3, m, k, k, "a"), _scales(a_scale, m, desc.a_scale_stride, "a_scale"),
-            _strided(b, DLF_FP8_E4M3, n, k, k, "b"), _scales(b_scale, slabs, desc.b_scale_stride, "b_scale"),
-            _sized(col_shift, _F32, 4 * n, "col_shift"))
-
-
 def dlf_gemm_blocks(desc, a, a_scale, b, b_scale, col_shift, residual, c, workspace, workspace_bytes, stream=None):
     """Product of e4m3 matrices whose rows have a scale for each 128 values of k, b's for each 128 rows
     (see include/dlfusion.h)."""
-    m, n = desc.m, desc.n
+    m, n, k = desc.m, desc.n, desc.k
+    shape = (m, n)
     workspace_bytes = int(workspace_bytes)
-    _check(_lib.dlf_gemm_blocks(ctypes.byref(desc),
-                                *_gemm_blocks_operands(desc, a, a_scale, b, b_scale, col_shift, -(-n // 128)),
-                                _strided(residual, DLF_BF16, m, n, n, "residual"),
-                                _strided(c, DLF_BF16, m, n, n, "c"),
-                                _workspace(workspace, workspace_bytes), workspace_bytes, _stream(stream)),
-           "dlf_gemm_blocks")
+    _check(_lib.dlf_gemm_blocks(ctypes.byref(desc), _strided(a, _FP8, (m, k), k, "a"),
+                                _scales(a_scale, m, desc.a_scale_stride, "a_scale"), _strided(b, _FP8, (n, k), k, "b"),
+                                _scales(b_scale, -(-n // 128), desc.b_scale_stride, "b_scale"),
+                                col_shift if col_shift is None else _scales(col_shift, 1, n, "col_shift"),
+                                residual if residual is None else _strided(residual, _BF16, shape, n, "residual"),
+                                _strided(c, _BF16, shape, n, "c"), _workspace(workspace, workspace_bytes),
+                                workspace_bytes, _stream(stream)), "dlf_gemm_blocks")
 
 
 def dlf_gemm_blocks_gated(desc, a, a_scale, b, b_scale, col_shift, gate, c, workspace, workspace_bytes, stream=None):
     """The same with interleaved gate and up rows: c[:, j] = gate(g_j) * u_j."""
-    m, n = desc.m, desc.n
+    m, n, k = desc.m, desc.n, desc.k
     workspace_bytes = int(workspace_bytes)
-    _check(_lib.dlf_gemm_blocks_gated(ctypes.byref(desc),
-                                      *_gemm_blocks_operands(desc, a, a_scale, b, b_scale, col_shift, 2 * -(-n // 256)),
-                                      GATES.get(gate, gate), _strided(c, DLF_BF16, m, n // 2, n // 2, "c"),
+    _check(_lib.dlf_gemm_blocks_gated(ctypes.byref(desc), _strided(a, _FP8, (m, k), k, "a"),
+                                      _scales(a_scale, m, desc.a_scale_stride, "a_scale"),
+                                      _strided(b, _FP8, (n, k), k, "b"),
+                                      _scales(b_scale, 2 * -(-n // 256), desc.b_scale_stride, "b_scale"),
+                                      col_shift if col_shift is None else _scales(col_shift, 1, n, "col_shift"),
+                                      GATES.get(gate, gate), _strided(c, _BF16, (m, n // 2), n // 2, "c"),
                                       _workspace(workspace, workspace_bytes), workspace_bytes, _stream(stream)),
            "dlf_gemm_blocks_gated")
 

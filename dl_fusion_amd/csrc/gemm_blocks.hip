@@ -5,8 +5,9 @@ namespace dlf {
 namespace {
 
 // A workgroup's tile: WM x WN waves, each of FM x FN fragments of 16 rows of a and 16 of b.
-template <int WM_, int WN_, int FM_, int FN_, int WAVES_ = 2>
+template <int WM_, int WN_, int FM_, int FN_, int STAGES_ = 2, int WAVES_ = 2>
 struct BlockTile {
+    static constexpr int STAGES = STAGES_;                      // blocks of k in LDS
     static constexpr int kWaves = WAVES_;                       // on a SIMD at least: its registers are shared by that many
     static constexpr int WM = WM_, WN = WN_, FM = FM_, FN = FN_;
     static constexpr int BM = 16 * WM * FM, BN = 16 * WN * FN;
@@ -20,7 +21,8 @@ struct BlockTile {
     static constexpr int kARow = WM * H * 64;                   // floats of a block
     static constexpr int kScales = (kGroup * kARow + 2 * kGroup) * 4;
     static constexpr int kOut = BM * BN * 2;                    // the staged output
-    static constexpr int kLds = 2 * kStage + 2 * kScales > kOut ? 2 * kStage + 2 * kScales : kOut;
+    static constexpr int kRing = STAGES * kStage;
+    static constexpr int kLds = kRing + 2 * kScales > kOut ? kRing + 2 * kScales : kOut;
     static_assert(FM % 4 == 0 && (LA + LB) % 4 == 0, "fragments and loads in turn");
     static_assert(LA >= 1 && LB >= 1 && BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && NW % 2 == 0, "whole loads");
     static_assert(BM % 64 == 0 && (BN == 128 || BN == 256 || BN == 64), "scales of whole waves, at most two rows of b's");
@@ -79,15 +81,15 @@ __global__ __launch_bounds__(T::NT, T::kWaves) void gemm_blocks_kernel(const Gem
     const int slabs = GATED ? slab + 2 : (p.n + kScaleBlock - 1) / kScaleBlock;
     const __amdgpu_buffer_rsrc_t rsb = buffer_rsrc(p.b_scale + static_cast<int64_t>(slab) * p.b_scale_stride,
                                                    static_cast<uint32_t>((slabs - slab < 2 ? slabs - slab : 2) * p.b_scale_stride * 4));
-    float* const scales = reinterpret_cast<float*>(lds + 2 * T::kStage);
+    float* const scales = reinterpret_cast<float*>(lds + T::kRing);
     constexpr int kLoads = T::LA + T::LB;
-    // load q of this wave's of block t, whose offset is `off`; past the last block and past k: zeros
+    // load q of this wave's of a block, whose offset is `off`, to a stage; past the last block and past k: zeros
     auto load_off = [&](int t) {
         const uint32_t at = static_cast<uint32_t>(begin + t) * kScaleBlock;
         return static_cast<int>(at) + 16 * chunk < k ? from + at : kOutOfRange;
     };
-    auto load_part = [&](int t, int q, uint32_t off) {
-        uint8_t* const to = lds + (t & 1) * T::kStage + wave * 1024;
+    auto load_part = [&](int stage, int q, uint32_t off) {
+        uint8_t* const to = lds + stage + wave * 1024;
         if (q < T::LA) load_lds16_buf(ra[q < T::LA ? q : 0], off, to + q * T::NW * 1024);
         else load_lds16_buf(rb[q < T::LA ? 0 : q - T::LA], off, to + T::BM * kScaleBlock + (q - T::LA) * T::NW * 1024);
     };
@@ -135,13 +137,15 @@ __global__ __launch_bounds__(T::NT, T::kWaves) void gemm_blocks_kernel(const Gem
     if (blocks > 0) {
         fetch_scales(0);
 #pragma unroll
-        for (int q = 0; q < kLoads; ++q) load_part(0, q, load_off(0));
+        for (int b = 0; b + 1 < T::STAGES; ++b)
+#pragma unroll
+            for (int q = 0; q < kLoads; ++q) load_part(b * T::kStage, q, load_off(b));
         keep_scales(0);
         fetch_scales(1);
-        wait_vmcnt<0>();
+        wait_vmcnt<(T::STAGES - 2) * kLoads>();
         barrier();
 #pragma unroll
-        for (int q = 0; q < kLoads / 2; ++q) load_part(1, q, load_off(1));
+        for (int q = 0; q < kLoads / 2; ++q) load_part((T::STAGES - 1) * T::kStage, q, load_off(T::STAGES - 1));
         // Fragments of a are read DEPTH groups of MFMAs ahead
         constexpr int DEPTH = 2, RING = 4;
         i32x8_t w[FN], x[RING];
@@ -167,6 +171,7 @@ __global__ __launch_bounds__(T::NT, T::kWaves) void gemm_blocks_kernel(const Gem
 #pragma unroll
         for (int j = 0; j < FN; ++j) part[(FM - 1) & 1][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
         float s0 = 0.0f, s1 = 0.0f;         // of the group whose sums are added next
+        int stage = 0;                      // of block t
         for (int t = 0; t < blocks;) {
             // The next kGroup blocks' scales into LDS, where those before the present ones have been used by all, and the ones
             // after on their way.  (Outside the loop below, whose body has to stay free of branches: the sums are moved
@@ -176,25 +181,25 @@ __global__ __launch_bounds__(T::NT, T::kWaves) void gemm_blocks_kernel(const Gem
             const int end = t + T::kGroup < blocks ? t + T::kGroup : blocks;
 #pragma unroll 1
             for (; t < end; ++t) {
-                const int stage = (t & 1) * T::kStage, next = T::kStage - stage;
-                const uint32_t off = load_off(t + 1), off2 = load_off(t + 2);
+                const int next = stage + T::kStage < T::kRing ? stage + T::kStage : 0, last = stage > 0 ? stage - T::kStage : T::kRing - T::kStage;
+                const uint32_t off = load_off(t + T::STAGES - 1), off2 = load_off(t + T::STAGES);
 #pragma unroll
                 for (int i = 0; i < FM; ++i) {
                     // A stage is left by all DEPTH groups before its block's end.  Half of its loads follow at once, half in
                     // the next block's first groups: spread over the MFMAs no wave waits for room in the queue of loads.
                     if (i < FM / 4) {
 #pragma unroll
-                        for (int q = 0; q < kLoads / (FM / 2); ++q) load_part(t + 1, kLoads / 2 + i * (kLoads / (FM / 2)) + q, off);
+                        for (int q = 0; q < kLoads / (FM / 2); ++q) load_part(last, kLoads / 2 + i * (kLoads / (FM / 2)) + q, off);
                     }
                     if (i + DEPTH == FM) {
                         // this wave's loads of the next block are there and its reads of this one done; after the barrier
                         // everyone's are
-                        wait_vmcnt<0>();
+                        wait_vmcnt<(T::STAGES - 2) * kLoads>();
                         barrier();
                     }
                     if (i + DEPTH >= FM) {
 #pragma unroll
-                        for (int q = 0; q < kLoads / 2 / DEPTH; ++q) load_part(t + 2, (i + DEPTH - FM) * (kLoads / 2 / DEPTH) + q, off2);
+                        for (int q = 0; q < kLoads / 2 / DEPTH; ++q) load_part(stage, (i + DEPTH - FM) * (kLoads / 2 / DEPTH) + q, off2);
                     }
                     const float t0 = s0, t1 = s1;
                     s0 = sa[i >> 2][i & 3] * b0;
@@ -229,6 +234,7 @@ __global__ __launch_bounds__(T::NT, T::kWaves) void gemm_blocks_kernel(const Gem
                     }
                     __builtin_amdgcn_sched_barrier(0);
                 }
+                stage = next;
             }
         }
 #pragma unroll
@@ -328,7 +334,7 @@ __global__ __launch_bounds__(T::NT, T::kWaves) void gemm_blocks_kernel(const Gem
 
 using Tile256 = BlockTile<2, 4, 8, 4>;      // 256 x 256, a wave 128 x 64
 using Tile128 = BlockTile<2, 2, 4, 4>;      // 128 x 128, a wave 64 x 64
-using Tile64 = BlockTile<1, 4, 4, 1, 4>;    // 64 x 64, a wave 64 x 16
+using Tile64 = BlockTile<1, 4, 4, 1, 3, 3>;    // 64 x 64, a wave 64 x 16
 
 template <class T, int ACT>
 hipError_t launch_tile(const GemmBlocksArgs& a, hipStream_t s) {
@@ -348,16 +354,17 @@ hipError_t launch(const GemmBlocksArgs& a, hipStream_t s) {
     }
 }
 
-// A workgroup that shares a CU with w - 1 others takes slope + share w us a block of k and `more` us besides (measured over 180
-// sizes, 48 to 8192 rows; on average the choice below is 1% slower than the best of all).
+// What a tile takes, in us: `more`, and for each block of k slope + share w + chip f, w workgroups on its CU and a share f of all
+// places of the chip taken.  Fitted to 180 sizes of 33 to 8192 rows, 300 to 22016 columns and sums of 1024 to 11008, each
+// measured with every tile and number of parts; the choice by it is 0.4% slower than the best on average, 16% at worst.
 struct TileCost {
     int kind, rows, cols, on_a_cu;
-    double slope, share, more;
+    double slope, share, chip, more;
 };
 constexpr TileCost kCosts[] = {
-    {kGemmBlocksTile64, 64, 64, 4, 0.31, 0.127, 0.2},
-    {kGemmBlocksTile128, 128, 128, 2, 0.40, 0.29, 1.0},
-    {kGemmBlocksTile256, 256, 256, 1, 0.0, 1.25, 4.0},
+    {kGemmBlocksTile64, 64, 64, 3, 0.13, 0.16, 0.0, 1.0},
+    {kGemmBlocksTile128, 128, 128, 2, 0.38, 0.32, 0.0, 1.2},
+    {kGemmBlocksTile256, 256, 256, 1, 1.2, 0.0, 0.35, 4.0},
 };
 
 }  // namespace
@@ -403,9 +410,10 @@ void plan_gemm_blocks(GemmBlocksArgs* a) {
             const int parts = cut(want, &blocks);
             if (parts != want || (parts > 1 && tiles >= 4 * kCus)) continue;
             const int64_t groups = tiles * parts, full = groups / (kCus * c.on_a_cu), rest = groups - full * kCus * c.on_a_cu;
-            double us = static_cast<double>(full) * (blocks * (c.slope + c.share * c.on_a_cu) + c.more);
-            if (rest > 0) us += blocks * (c.slope + c.share * static_cast<double>((rest + kCus - 1) / kCus)) + c.more;
-            if (parts > 1) us += 2.0 + parts * static_cast<double>(a->m) * a->n * 8 / 5.6e6;
+            double us = static_cast<double>(full) * (blocks * (c.slope + c.share * c.on_a_cu + c.chip) + c.more);
+            if (rest > 0)
+                us += blocks * (c.slope + c.share * static_cast<double>((rest + kCus - 1) / kCus) + c.chip * static_cast<double>(rest) / (kCus * c.on_a_cu)) + c.more;
+            if (parts > 1) us += 2.0 + parts * static_cast<double>(a->m) * a->n * 8 / 5.5e6;
             if (best == 0 || us < best) {
                 best = us;
                 a->kind = c.kind;
