@@ -1,9 +1,10 @@
 """One attention block of a decoding model over a paged key-value cache, run through the C ABI.
 
-The block is  y = x + attention(x W_qkv^T [+ adapters]) W_o^T  for requests whose keys and values live in
-pages of one pool.  A step enqueues, on the current stream and without reading anything back:
+The block is  y = x + attention(n W_qkv^T [+ adapters]) W_o^T,  n = x or its root-mean-square norm, for requests whose
+keys and values live in pages of one pool.  A step enqueues, on the current stream and without reading anything back:
 
     dlf_page_plan        pages and slots for the step's tokens, from the lengths on the device
+    dlf_rms_norm         the norm, if there is one
     dlf_gemm_fused       queries, keys and values in one product
     dlf_lora_add         each request's adapter on it, in place
     dlf_paged_store      the new keys and values into their slots, out of the product's columns
@@ -20,8 +21,8 @@ from __future__ import annotations
 import torch
 
 from . import (dlf_gemm_fused, dlf_lora_add, dlf_lora_workspace_bytes, dlf_page_plan, dlf_paged_attention,
-               dlf_paged_attention_workspace_bytes, dlf_paged_store, gemm_desc, kv_cache_desc, lora_desc,
-               page_plan_desc, paged_attn_desc)
+               dlf_paged_attention_workspace_bytes, dlf_paged_store, dlf_rms_norm, gemm_desc, kv_cache_desc, lora_desc,
+               page_plan_desc, paged_attn_desc, rms_norm_desc)
 
 
 def _shaped(t, shape, name, dtype=torch.bfloat16):
@@ -33,12 +34,12 @@ def _shaped(t, shape, name, dtype=torch.bfloat16):
 class PagedAttentionBlock:
     """``w_qkv`` [(heads + 2 kv_heads) * head_dim][hidden] (queries, keys, values) and ``w_o``
     [hidden][heads * head_dim], bf16 on the device.  ``adapters``: (a [count][rank][hidden],
-    b [count][qkv columns][rank], scale [count] or None) or None.  A pool of ``pages`` pages is shared by
-    ``requests`` places of up to ``max_pages`` pages each."""
+    b [count][qkv columns][rank], scale [count] or None) or None.  ``norm``: (weight fp32 [hidden] or None, eps) or
+    None.  A pool of ``pages`` pages is shared by ``requests`` places of up to ``max_pages`` pages each."""
 
     def __init__(self, w_qkv, w_o, heads, kv_heads, head_dim, requests, pages, page_size, max_pages, adapters=None,
-                 cache="bf16", k_scale=1.0, v_scale=1.0, max_len=0):
-        self.w_qkv, self.w_o, self.adapters = w_qkv, w_o, adapters
+                 cache="bf16", k_scale=1.0, v_scale=1.0, max_len=0, norm=None):
+        self.w_qkv, self.w_o, self.adapters, self.norm = w_qkv, w_o, adapters, norm
         self.heads, self.kv_heads, self.head_dim, self.requests = heads, kv_heads, head_dim, requests
         self.page_size, self.max_pages = page_size, max_pages
         self.width, self.hidden = w_qkv.shape
@@ -51,6 +52,8 @@ class PagedAttentionBlock:
             _shaped(b, (count, self.width, rank), "the adapters' b")
             if scale is not None:
                 _shaped(scale, (count,), "the adapters' scale", torch.float32)
+        if norm is not None and norm[0] is not None:
+            _shaped(norm[0], (self.hidden,), "the norm's weight", torch.float32)
         device = w_qkv.device
         i32 = dict(dtype=torch.int32, device=device)
         self.cache = kv_cache_desc(pages, kv_heads, page_size, head_dim, cache, k_scale, v_scale)
@@ -105,17 +108,23 @@ class PagedAttentionBlock:
         return dict(slots=torch.empty(m, dtype=torch.int64, device=device),
                     rows=torch.empty(m, dtype=torch.int32, device=device),
                     qkv=torch.empty(m, self.width, dtype=torch.bfloat16, device=device),
+                    normed=torch.empty(m if self.norm is not None else 0, self.hidden, dtype=torch.bfloat16, device=device),
                     lora_ws=torch.empty(lora_ws, dtype=torch.uint8, device=device))
 
     def _views(self, m, room):
         got = dict(plan=page_plan_desc(self.requests, self.page_size, self.max_pages, m, self.free.numel()),
                    product=gemm_desc(m, self.width, self.hidden), lora_ws=room["lora_ws"],
-                   **{n: room[n][:m] for n in ("slots", "rows", "qkv")})
+                   **{n: room[n][:m] for n in ("slots", "rows", "qkv", "normed")})
+        if self.norm is not None:
+            got["norm"] = rms_norm_desc(m, self.hidden, self.norm[1])
         if self.adapters is not None:
             got["lora"] = self._lora(m)[0]
         return got
 
     def _project(self, x, b, row_map):
+        if self.norm is not None:
+            dlf_rms_norm(b["norm"], x, None, self.norm[0], None, b["normed"], None)
+            x = b["normed"]
         dlf_gemm_fused(b["product"], x, self.w_qkv, None, None, None, b["qkv"])
         if self.adapters is not None:
             a, up, scale = self.adapters
@@ -205,6 +214,8 @@ def main():
     ap.add_argument("--steps", type=int, default=64)
     ap.add_argument("--cache", choices=["bf16", "fp8"], default="bf16")
     ap.add_argument("--adapters", type=int, default=8)
+    ap.add_argument("--feed-forward", type=int, default=0, metavar="D_FF",
+                    help="a whole layer: norms, and a gated feed-forward block of this width on 8-bit weights")
     a = ap.parse_args()
     hidden, heads, kv_heads, dim, page, rank = 4096, 32, 8, 128, 16, 16
     g = torch.Generator(device="cuda").manual_seed(0)
@@ -219,7 +230,19 @@ def main():
         adapters = (rand(a.adapters, rank, hidden, scale=hidden ** -0.5), rand(a.adapters, width, rank, scale=0.1), None)
     block = PagedAttentionBlock(rand(width, hidden, scale=hidden ** -0.5), rand(hidden, heads * dim, scale=hidden ** -0.5),
                                 heads, kv_heads, dim, a.requests, a.requests * max_pages, page, max_pages, adapters,
-                                cache=a.cache, k_scale=0.0625, v_scale=0.0625, max_len=max_pages * page)
+                                cache=a.cache, k_scale=0.0625, v_scale=0.0625, max_len=max_pages * page,
+                                norm=(None, 1e-5) if a.feed_forward else None)
+    layer = block.step
+    if a.feed_forward:
+        from .feed_forward import GatedFeedForward, pack, pack_gate_up
+        gate, up = (rand(a.feed_forward, hidden, scale=hidden ** -0.5).float().cpu() for _ in range(2))
+        down = rand(hidden, a.feed_forward, scale=a.feed_forward ** -0.5).float().cpu()
+        feed_forward = GatedFeedForward(pack_gate_up(gate, up), pack(down), rows=a.requests)
+        middle = torch.empty(a.requests, hidden, dtype=torch.bfloat16, device="cuda")
+
+        def layer(x, fresh, y):
+            block.step(x, fresh, middle)
+            feed_forward(middle, y)
     if a.adapters:
         block.ids.copy_(torch.arange(a.requests) % a.adapters)
     prompts = [max(1, a.prompt * (i + 1) // a.requests) for i in range(a.requests)]
@@ -227,11 +250,11 @@ def main():
     block.admit(rand(sum(prompts), hidden), fresh)
     x, y = rand(a.requests, hidden), torch.empty(a.requests, hidden, dtype=torch.bfloat16, device="cuda")
     one = torch.ones(a.requests, dtype=torch.int32, device="cuda")
-    block.step(x, one, y)
+    layer(x, one, y)
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        block.step(x, one, y)
+        layer(x, one, y)
     begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
     begin.record()
     for _ in range(a.steps):

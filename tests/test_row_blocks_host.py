@@ -308,3 +308,26 @@ def test_weights_refusals():
 def test_weights_of_zeros():
     codes, scale = dlf.dlf_quant_blocks_weights(np.zeros((2, 16), np.float32))
     assert (codes == 0).all() and scale[0, 0] == np.float32(2.0 ** -110 / 448) and (scale[0, 1:] == 0).all()
+
+
+# ---------------------------------------------------------------------------
+# The feed-forward block's weights
+# ---------------------------------------------------------------------------
+def test_feed_forward_packs_and_refuses():
+    from dl_fusion_amd.feed_forward import GatedFeedForward, pack, pack_gate_up
+    r = np.random.RandomState(0)
+    gate, up, down = (r.randn(*s).astype(np.float32) for s in ((300, 256), (300, 256), (256, 304)))
+    codes, scale = pack_gate_up(gate, up, "cpu")
+    # row j of the gate is row 2j, of the up weight row 2j + 1, each with the scale that it has alone
+    for w, first in ((gate, 0), (up, 1)):
+        c, s = dlf.dlf_quant_blocks_weights(w)
+        assert torch.equal(codes.view(torch.uint8)[first::2], torch.from_numpy(c)) and torch.equal(scale[first::2], torch.from_numpy(s))
+    with pytest.raises(ValueError):
+        pack_gate_up(gate, up[:299], "cpu")
+    down = pack(down[:, :300 // 16 * 16], "cpu")
+    small = pack_gate_up(gate[:288], up[:288], "cpu")
+    GatedFeedForward(small, down)
+    for bad in (dict(gate_up=down), dict(down=small), dict(norm=torch.ones(255)), dict(norm=torch.ones(256).double()),
+                dict(gate_up=(small[0], small[1][:1])), dict(gate_up=(small[0].view(torch.uint8), small[1]))):
+        with pytest.raises(ValueError):
+            GatedFeedForward(**{**dict(gate_up=small, down=down), **bad})
