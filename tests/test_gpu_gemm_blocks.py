@@ -170,6 +170,43 @@ def test_large(m, n, k, gate):
     check(make(m, n, k, gate is not None), gate=gate)
 
 
+@pytest.mark.parametrize("m", [1, 16, 17, 32])
+@pytest.mark.parametrize("n", [6144, 6146, 6161, 8200])
+def test_few_rows_and_many_columns(m, n):
+    check(make(m, n, 272, shift=True, residual=True))
+    if n % 2 == 0:
+        check(make(m, n, 384, True), gate="silu")
+
+
+@pytest.mark.parametrize("m,n,k,gate", [(1, 256, 11008, None), (20, 301, 11008, None), (32, 1026, 8192, "gelu_tanh"), (33, 5, 8192, None),
+                                        (50, 1023, 8192, None), (40, 514, 8208, "silu"), (300, 130, 20480, None), (129, 258, 5000 // 16 * 16, "silu"),
+                                        (64, 2048, 4096, None), (200, 700, 16384, None), (1000, 256, 8192, None)])
+def test_sums_in_parts(m, n, k, gate):
+    import dl_fusion_amd as dl
+    assert dl.dlf_gemm_blocks_workspace_bytes(dl.gemm_blocks_desc(m, n, k)) > 0
+    s = make(m, n, k, gate is not None, shift=True, residual=gate is None)
+    check(s, "none" if gate else "gelu_tanh", gate)
+
+
+def test_two_streams_at_once():
+    import dl_fusion_amd as dl
+    cases = [(make(m, n, k, seed=i), dl.gemm_blocks_desc(m, n, k)) for i, (m, n, k) in
+             enumerate([(64, 4096, 11008), (500, 2048, 2048), (16, 4096, 4096), (300, 1024, 8192)])]
+    want = [product(s) for s, _ in cases]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [torch.empty_like(w) for w in want]
+    ws = [torch.empty(dl.dlf_gemm_blocks_workspace_bytes(d), dtype=torch.uint8, device="cuda") for _, d in cases]
+    torch.cuda.synchronize()
+    for turn in range(3):
+        for i, (s, d) in enumerate(cases):
+            dl.dlf_gemm_blocks(d, s["a"], s["a_scale"], s["b"], s["b_scale"], None, None, got[i], ws[i], ws[i].numel(), streams[i % 2])
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert torch.equal(g, w)
+            g.zero_()
+        torch.cuda.synchronize()
+
+
 @pytest.mark.parametrize("m,n,k,gate", [(9, 300, 1024, None), (80, 300, 400, None), (400, 512, 1024, "silu"), (900, 768, 256, None)])
 def test_codes_of_all_magnitudes(m, n, k, gate):
     check(make(m, n, k, gate is not None, whole=False), gate=gate)
