@@ -73,7 +73,8 @@ extern "C" dlf_status dlf_rms_norm(const dlf_rms_norm_desc* d, const void* x, co
     dlf_status st = check_rows(d->rows, d->cols, d->dtype);
     if (st != DLF_OK) return st;
     if (!known(d->out_dtype)) return fail(DLF_ERR_INVALID_ARG, "unknown dtype");
-    if (!std::isfinite(d->eps) || d->eps <= 0.0f) return fail(DLF_ERR_INVALID_ARG, "eps must be finite and > 0");
+    // below, squares that fp32 holds with fewer bits, or not at all, would count beside it
+    if (!std::isfinite(d->eps) || d->eps < 0x1p-100f) return fail(DLF_ERR_INVALID_ARG, "eps must be finite and at least 2^-100");
     if ((st = check_stride(d->x_stride, d->cols)) != DLF_OK || (st = check_stride(d->y_stride, d->cols)) != DLF_OK) return st;
     if (residual && (st = check_stride(d->residual_stride, d->cols)) != DLF_OK) return st;
     if (sum && (st = check_stride(d->sum_stride, d->cols)) != DLF_OK) return st;

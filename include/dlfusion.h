@@ -416,7 +416,7 @@ typedef struct {
     int64_t x_stride, residual_stride, sum_stride, y_stride;
     dlf_dtype dtype;            /* x, residual and sum: BF16 or F32 */
     dlf_dtype out_dtype;        /* y: BF16, F32 or FP8_E4M3 */
-    float eps;                  /* finite, > 0 */
+    float eps;                  /* finite, >= 2^-100 */
     float out_inv_scale;        /* FP8_E4M3 without y_scale: fp32(1 / s_y), finite and > 0 */
 } dlf_rms_norm_desc;
 

@@ -231,6 +231,28 @@ def test_norm_of_rows_that_are_not_finite(cols):
     assert torch.isfinite(c).all()
 
 
+def test_rows_past_4_gigabytes():
+    """Four rows 2^30 + 8 elements apart, of the norm and of the quantiser."""
+    import dl_fusion_amd as dl
+    rows, cols, stride = 4, 4096, (1 << 30) + 8
+    x, r = rows_of(rows, cols, "bf16", 20), rows_of(rows, cols, "bf16", 21)
+    s0, y0, c0 = norm(x, r, None, "blocks", True)
+    q0, qs0 = quant(x)
+    far = [torch.empty(rows * stride, dtype=torch.bfloat16, device="cuda").view(rows, stride)[:, :cols] for _ in range(3)]
+    codes = [torch.empty(rows * stride, dtype=torch.uint8, device="cuda").view(FP8).view(rows, stride)[:, :cols] for _ in range(2)]
+    far[0].copy_(x)
+    far[1].copy_(r)
+    c, qs = torch.empty(rows, 32, device="cuda"), torch.empty(rows, 32, device="cuda")
+    dl.dlf_rms_norm(dl.rms_norm_desc(rows, cols, EPS, "bf16", "fp8", 1.0, stride, stride, stride, stride), far[0], far[1], None,
+                    far[2], codes[0], c)
+    dl.dlf_quant_blocks(dl.quant_blocks_desc(rows, cols, "bf16", stride, stride), far[0], codes[1], qs)
+    torch.cuda.synchronize()
+    for got, want in ((far[2], s0), (c, c0), (qs, qs0)):
+        assert torch.equal(got.cpu(), want)
+    for got, want in zip(codes, (y0, q0)):
+        assert torch.equal(got.view(torch.uint8).cpu(), want.view(torch.uint8))
+
+
 def test_norm_of_zeros():
     for out in ("bf16", "blocks"):
         _, y, c = norm(torch.zeros(3, 300, dtype=torch.bfloat16), None, None, out, True)

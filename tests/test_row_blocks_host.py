@@ -36,7 +36,7 @@ def call_norm(x=addr(0), residual=addr(1), weight=addr(2), sum=addr(3), y=addr(4
 @fake_pointers
 @pytest.mark.parametrize("kw,status", [
     (dict(rows=-1), INVALID), (dict(cols=0), INVALID), (dict(cols=-8), INVALID), (dict(dtype=7), INVALID),
-    (dict(out_dtype=-1), INVALID), (dict(dtype="fp8"), UNSUPPORTED), (dict(eps=0.0), INVALID), (dict(eps=-1e-5), INVALID),
+    (dict(out_dtype=-1), INVALID), (dict(dtype="fp8"), UNSUPPORTED), (dict(eps=0.0), INVALID), (dict(eps=-1e-5), INVALID), (dict(eps=7e-31), INVALID),
     (dict(eps=NAN), INVALID), (dict(eps=INF), INVALID), (dict(x_stride=255), INVALID), (dict(residual_stride=255), INVALID),
     (dict(sum_stride=0), INVALID), (dict(y_stride=-256), INVALID), (dict(x_stride=(1 << 31) + 1), UNSUPPORTED),
     (dict(y_stride=(1 << 31) + 1), UNSUPPORTED), (dict(cols=(1 << 23) + 1), UNSUPPORTED), (dict(rows=1 << 31), UNSUPPORTED),
