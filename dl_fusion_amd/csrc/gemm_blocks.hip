@@ -23,7 +23,7 @@ struct BlockTile {
     static constexpr int kOut = BM * BN * 2;                    // the staged output
     static constexpr int kRing = STAGES * kStage;
     static constexpr int kLds = kRing + 2 * kScales > kOut ? kRing + 2 * kScales : kOut;
-    static_assert(FM % 4 == 0 && (LA + LB) % 4 == 0, "fragments and loads in turn");
+    static_assert(FM % 4 == 0 && NW == FM && LA % 2 == 0 && (LA + LB) % FM == 0, "a load of a is half of a wave's rows; the loads go evenly into the groups");
     static_assert(LA >= 1 && LB >= 1 && BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && NW % 2 == 0, "whole loads");
     static_assert(BM % 64 == 0 && (BN == 128 || BN == 256 || BN == 64), "scales of whole waves, at most two rows of b's");
 };
@@ -83,15 +83,20 @@ __global__ __launch_bounds__(T::NT, T::kWaves) void gemm_blocks_kernel(const Gem
                                                    static_cast<uint32_t>((slabs - slab < 2 ? slabs - slab : 2) * p.b_scale_stride * 4));
     float* const scales = reinterpret_cast<float*>(lds + T::kRing);
     constexpr int kLoads = T::LA + T::LB;
-    // load q of this wave's of a block, whose offset is `off`, to a stage; past the last block and past k: zeros
     auto load_off = [&](int t) {
         const uint32_t at = static_cast<uint32_t>(begin + t) * kScaleBlock;
         return static_cast<int>(at) + 16 * chunk < k ? from + at : kOutOfRange;
     };
+    // Load q of this wave's of a block, whose offset is `off`, to a stage: b's, then those of a's with the first halves of the
+    // waves' rows, which are wanted first, then the second halves'.  Past the last block and past k: zeros.
     auto load_part = [&](int stage, int q, uint32_t off) {
         uint8_t* const to = lds + stage + wave * 1024;
-        if (q < T::LA) load_lds16_buf(ra[q < T::LA ? q : 0], off, to + q * T::NW * 1024);
-        else load_lds16_buf(rb[q < T::LA ? 0 : q - T::LA], off, to + T::BM * kScaleBlock + (q - T::LA) * T::NW * 1024);
+        if (q < T::LB) {
+            load_lds16_buf(rb[q < T::LB ? q : 0], off, to + T::BM * kScaleBlock + q * T::NW * 1024);
+        } else {
+            const int h = q - T::LB, j = h < T::LA / 2 ? 2 * h : 2 * (h - T::LA / 2) + 1;
+            load_lds16_buf(ra[q < T::LB ? 0 : j], off, to + j * T::NW * 1024);
+        }
     };
     // Scales of the blocks kGroup u ..: two lanes a row and 16 bytes a lane, through registers, since LDS wants them in
     // another order.  What lies past a row's last block is never used.
@@ -134,6 +139,16 @@ __global__ __launch_bounds__(T::NT, T::kWaves) void gemm_blocks_kernel(const Gem
 #pragma unroll
         for (int i = 0; i < FM; ++i) acc[j][i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
+    // A block is FM groups of FN MFMAs.  With many groups its place in LDS comes free in two steps: b's rows and the first halves
+    // of the waves' rows of a with group kHalf, when all have read them, the second halves DEPTH groups before the end; the loads
+    // of the block that is to lie there follow as evenly as the MFMAs, kEach a group, so that they find no queue and each has more
+    // than a block's time, and the same two barriers say that the loads that are read next have landed.  With few groups a second
+    // barrier costs more than it gives: all comes free DEPTH groups before the end, half of the loads follow at once, half in the
+    // next block's first group.  (us, one step | two, with inputs that no cache holds: 8192 x 22016 x 4096 gated 651 | 627,
+    // 8192 x 4096 x 11008 316 | 299; 777 x 5000 x 4112, four groups, 34.3 | 38.5.)
+    constexpr int DEPTH = 2, RING = 4;      // fragments of a are read DEPTH groups of MFMAs ahead
+    constexpr bool kTwice = FM >= 8;
+    constexpr int kHalf = FM / 2 - 2, kEach = kLoads / FM;
     if (blocks > 0) {
         fetch_scales(0);
 #pragma unroll
@@ -145,9 +160,7 @@ __global__ __launch_bounds__(T::NT, T::kWaves) void gemm_blocks_kernel(const Gem
         wait_vmcnt<(T::STAGES - 2) * kLoads>();
         barrier();
 #pragma unroll
-        for (int q = 0; q < kLoads / 2; ++q) load_part((T::STAGES - 1) * T::kStage, q, load_off(T::STAGES - 1));
-        // Fragments of a are read DEPTH groups of MFMAs ahead
-        constexpr int DEPTH = 2, RING = 4;
+        for (int q = 0; q < (kTwice ? kLoads - kHalf * kEach : kLoads / 2); ++q) load_part((T::STAGES - 1) * T::kStage, q, load_off(T::STAGES - 1));
         i32x8_t w[FN], x[RING];
         f32x4_t sa[T::H];                   // scales of the rows of four fragments
         float b0, b1;                       // of the wave's columns, even and odd
@@ -182,24 +195,30 @@ __global__ __launch_bounds__(T::NT, T::kWaves) void gemm_blocks_kernel(const Gem
 #pragma unroll 1
             for (; t < end; ++t) {
                 const int next = stage + T::kStage < T::kRing ? stage + T::kStage : 0, last = stage > 0 ? stage - T::kStage : T::kRing - T::kStage;
-                const uint32_t off = load_off(t + T::STAGES - 1), off2 = load_off(t + T::STAGES);
+                const uint32_t off_last = load_off(t + T::STAGES - 1), off = load_off(t + T::STAGES);
 #pragma unroll
                 for (int i = 0; i < FM; ++i) {
-                    // A stage is left by all DEPTH groups before its block's end.  Half of its loads follow at once, half in
-                    // the next block's first groups: spread over the MFMAs no wave waits for room in the queue of loads.
-                    if (i < FM / 4) {
-#pragma unroll
-                        for (int q = 0; q < kLoads / (FM / 2); ++q) load_part(last, kLoads / 2 + i * (kLoads / (FM / 2)) + q, off);
-                    }
-                    if (i + DEPTH == FM) {
-                        // this wave's loads of the next block are there and its reads of this one done; after the barrier
-                        // everyone's are
-                        wait_vmcnt<(T::STAGES - 2) * kLoads>();
+                    if (kTwice && i == kHalf) {
+                        wait_vmcnt<(T::STAGES - 1) * kLoads>();
                         barrier();
                     }
-                    if (i + DEPTH >= FM) {
+                    if (i == FM - DEPTH) {
+                        wait_vmcnt<(T::STAGES - 2) * kLoads + (kTwice ? T::LA / 2 + (FM - DEPTH - kHalf) * kEach : 0)>();
+                        barrier();
+                    }
+                    // loads of block t + STAGES to this one's place, or the rest of the last one's
+                    if (kTwice) {
 #pragma unroll
-                        for (int q = 0; q < kLoads / 2 / DEPTH; ++q) load_part(stage, (i + DEPTH - FM) * (kLoads / 2 / DEPTH) + q, off2);
+                        for (int q = 0; q < kEach; ++q) {
+                            if (i >= kHalf) load_part(stage, (i - kHalf) * kEach + q, off);
+                            else load_part(last, (i - kHalf + FM) * kEach + q, off_last);
+                        }
+                    } else if (i >= FM - DEPTH) {
+#pragma unroll
+                        for (int q = 0; q < kLoads / 4; ++q) load_part(stage, (i - FM + DEPTH) * (kLoads / 4) + q, off);
+                    } else if (i == 0) {
+#pragma unroll
+                        for (int q = kLoads / 2; q < kLoads; ++q) load_part(last, q, off_last);
                     }
                     const float t0 = s0, t1 = s1;
                     s0 = sa[i >> 2][i & 3] * b0;
@@ -227,7 +246,8 @@ __global__ __launch_bounds__(T::NT, T::kWaves) void gemm_blocks_kernel(const Gem
 #pragma unroll
                     for (int j = 0; j < FN; ++j) {
                         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                        if ((i < FM / 4 || i + DEPTH >= FM) && j % 2 == 0) __builtin_amdgcn_sched_group_barrier(0x020, kLoads >= 8 ? kLoads / 8 : 1, 0);
+                        if (kTwice ? j < kEach : j % 2 == 0 && (i == 0 || i >= FM - DEPTH))
+                            __builtin_amdgcn_sched_group_barrier(0x020, kTwice || kLoads < 8 ? 1 : kLoads / 8, 0);
                         if (i + 1 == FM) __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
                         else __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
                         __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);
@@ -245,6 +265,7 @@ __global__ __launch_bounds__(T::NT, T::kWaves) void gemm_blocks_kernel(const Gem
 
     // a part of the sum goes to the workspace as it is
     if (p.parts > 1) {
+        wait_vmcnt<0>();        // the last loads are on their way to LDS yet
 #pragma unroll
         for (int j = 0; j < FN; ++j)
 #pragma unroll
