@@ -8,8 +8,8 @@ without reading anything back:
     dlf_quant_blocks        the activations into codes and scales
     dlf_gemm_blocks         the down projection with the residual
 
-so that it can be captured in a graph.  The weights take half of what bf16 does, and where there are few rows, as in a
-step of decoding, half of the time.
+so that it can be captured in a graph.  The weights take half of what bf16 does; where there are few rows, as in a step
+of decoding, their read is what a call takes.
 """
 from __future__ import annotations
 
@@ -53,7 +53,8 @@ def _packed(w, rows, cols, scale_rows, name):
 class GatedFeedForward:
     """``gate_up`` and ``down``: what pack_gate_up and pack return.  ``norm``: fp32 [d_model] or None (= 1).
     ``rows``: rows of a call that may be captured: their buffers are made here and stay where they are.  Calls of other
-    lengths share one set of buffers, which grows to the longest."""
+    lengths share one set of buffers, which grows to the longest, and are refused under capture.  A set is one call's at a
+    time: calls on streams that overlap need a block each (the weights may be the same tensors)."""
 
     def __init__(self, gate_up, down, norm=None, eps=1e-5, gate="silu", rows=0):
         self.gate_up, self.down, self.norm, self.eps, self.gate = gate_up, down, norm, eps, gate
@@ -90,6 +91,8 @@ class GatedFeedForward:
     def _buffers(self, m):
         if m == self.rows and self._own is not None:
             return self._own
+        if torch.cuda.is_current_stream_capturing():
+            raise ValueError(f"only calls of `rows` = {self.rows} rows may be captured, got {m}")
         need = max(dlf_gemm_blocks_workspace_bytes(d) for d in self._descs(m))
         if self._shared is None or self._shared["x"].shape[0] < m or self._shared["ws"].numel() < need:
             most, ws = (0, 0) if self._shared is None else (self._shared["x"].shape[0], self._shared["ws"].numel())

@@ -66,7 +66,7 @@ def test_stage_by_stage(m, d_model, d_ff, gate, norm):
 
 
 def test_captured_beside_calls_of_other_lengths():
-    block, _ = build(512, 1536, rows=40)
+    block, _ = build(512, 1408, rows=40)
     x = rows_of(40, 512, 3)
     y = torch.empty_like(x)
     block(x, y)
@@ -91,6 +91,21 @@ def test_captured_beside_calls_of_other_lengths():
         block(long, first)
         torch.cuda.synchronize()
         assert torch.equal(first, other)
+
+
+def test_a_call_that_shares_its_buffers_is_refused_under_capture():
+    block, _ = build(256, 512, rows=8)
+    x = rows_of(9, 256, 1)
+    y = torch.zeros_like(x)
+    block(x, y)
+    torch.cuda.synchronize()
+    want = y.clone()
+    graph = torch.cuda.CUDAGraph()
+    with pytest.raises(ValueError), torch.cuda.graph(graph):
+        block(x, y)
+    block(x, y)
+    torch.cuda.synchronize()
+    assert torch.equal(y, want)
 
 
 def test_no_rows():
