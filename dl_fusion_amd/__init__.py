@@ -592,6 +592,18 @@ def _refuse_strided(t, dtype, shape, stride, name):
         raise ValueError(f"{name} must be [{rows}][{cols}] with rows {stride} elements apart")
 
 
+def _stream_of(stream, x, y):
+    """The stream's handle.  A call on the current stream is the current device's: x and y, the first input and the output,
+    have to lie there, since a kernel would fault on another's memory."""
+    if stream is not None:
+        return _stream(stream)
+    here = torch.cuda.current_device()
+    for t in (x, y):
+        if t.__class__ is not int and t is not None and t.get_device() != here:
+            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{here}")
+    return torch._C._cuda_getCurrentRawStream(here)
+
+
 def _scales(t, rows, stride, name):
     """Device pointer of contiguous fp32 block scales [rows][stride], or of a raw address or None as it is."""
     if t is None or t.__class__ is int:
@@ -612,7 +624,7 @@ def dlf_rms_norm(desc, x, residual, weight, sum, y, y_scale, stream=None):
                              sum if sum is None else _strided(sum, dtype, shape, desc.sum_stride, "sum"),
                              _strided(y, _TYPES.get(desc.out_dtype), shape, desc.y_stride, "y"),
                              y_scale if y_scale is None else _scales(y_scale, n, desc.scale_stride, "y_scale"),
-                             _stream(stream)), "dlf_rms_norm")
+                             _stream_of(stream, x, y)), "dlf_rms_norm")
 
 
 def dlf_quant_blocks(desc, x, codes, scale, stream=None):
@@ -620,7 +632,7 @@ def dlf_quant_blocks(desc, x, codes, scale, stream=None):
     shape = desc.rows, desc.cols
     _check(_lib.dlf_quant_blocks(ctypes.byref(desc), _strided(x, _TYPES.get(desc.dtype), shape, desc.x_stride, "x"),
                                  _strided(codes, _FP8, shape, desc.codes_stride, "codes"),
-                                 _scales(scale, shape[0], desc.scale_stride, "scale"), _stream(stream)),
+                                 _scales(scale, shape[0], desc.scale_stride, "scale"), _stream_of(stream, x, codes)),
            "dlf_quant_blocks")
 
 
@@ -642,7 +654,7 @@ def dlf_gemm_blocks(desc, a, a_scale, b, b_scale, col_shift, residual, c, worksp
                                 col_shift if col_shift is None else _scales(col_shift, 1, n, "col_shift"),
                                 residual if residual is None else _strided(residual, _BF16, shape, n, "residual"),
                                 _strided(c, _BF16, shape, n, "c"), _workspace(workspace, workspace_bytes),
-                                workspace_bytes, _stream(stream)), "dlf_gemm_blocks")
+                                workspace_bytes, _stream_of(stream, a, c)), "dlf_gemm_blocks")
 
 
 def dlf_gemm_blocks_gated(desc, a, a_scale, b, b_scale, col_shift, gate, c, workspace, workspace_bytes, stream=None):
@@ -655,7 +667,7 @@ def dlf_gemm_blocks_gated(desc, a, a_scale, b, b_scale, col_shift, gate, c, work
                                       _scales(b_scale, 2 * -(-n // 256), desc.b_scale_stride, "b_scale"),
                                       col_shift if col_shift is None else _scales(col_shift, 1, n, "col_shift"),
                                       GATES.get(gate, gate), _strided(c, _BF16, (m, n // 2), n // 2, "c"),
-                                      _workspace(workspace, workspace_bytes), workspace_bytes, _stream(stream)),
+                                      _workspace(workspace, workspace_bytes), workspace_bytes, _stream_of(stream, a, c)),
            "dlf_gemm_blocks_gated")
 
 
