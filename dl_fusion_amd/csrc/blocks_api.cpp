@@ -23,6 +23,7 @@ using dlf::Span;
 
 constexpr int32_t kMaxCols = 1 << 23;
 constexpr int64_t kMaxStride = int64_t(1) << 31;
+constexpr int32_t kMaxScaleStride = 1 << 20;     // 256 rows of scales are below 2^31 bytes, a buffer's size
 
 bool known(dlf_dtype d) { return d == DLF_F32 || d == DLF_BF16 || d == DLF_FP8_E4M3; }
 size_t size_of(dlf_dtype d) { return d == DLF_F32 ? 4 : d == DLF_BF16 ? 2 : 1; }
@@ -47,6 +48,7 @@ dlf_status check_stride(int64_t stride, int64_t width) {
 dlf_status check_scale_stride(int32_t stride, int64_t cols) {
     if (stride < blocks_of(cols)) return fail(DLF_ERR_INVALID_ARG, "a row of scales has fewer entries than the row has blocks");
     if (stride % 4 != 0) return fail(DLF_ERR_UNSUPPORTED, "scale strides must be multiples of 4");
+    if (stride > kMaxScaleStride) return fail(DLF_ERR_UNSUPPORTED, "scale strides must be at most 2^20");
     return ok();
 }
 
@@ -166,8 +168,8 @@ dlf_status check_gemm_desc(const dlf_gemm_blocks_desc* d, dlf::GemmBlocksArgs* g
         return fail(DLF_ERR_INVALID_ARG, "unknown activation %d", static_cast<int>(d->act));
     if (d->m < 0 || d->n < 0 || d->k < 0) return fail(DLF_ERR_INVALID_ARG, "negative dimension");
     if (d->k % 16 != 0) return fail(DLF_ERR_UNSUPPORTED, "k must be a multiple of 16");
-    if (d->n > kMaxCols || d->k > kMaxCols || d->m > (int64_t(1) << 24) || d->m * d->n >= (int64_t(1) << 38))
-        return fail(DLF_ERR_UNSUPPORTED, "n and k must be at most 2^23, m at most 2^24, m * n below 2^38");
+    if (d->n > kMaxCols || d->k > kMaxCols || d->m > (int64_t(1) << 24) || d->m * d->n >= (int64_t(1) << 37))
+        return fail(DLF_ERR_UNSUPPORTED, "n and k must be at most 2^23, m at most 2^24, m * n below 2^37");
     dlf_status st = check_scale_stride(d->a_scale_stride, d->k);
     if (st != DLF_OK || (st = check_scale_stride(d->b_scale_stride, d->k)) != DLF_OK) return st;
     *g = dlf::GemmBlocksArgs{};

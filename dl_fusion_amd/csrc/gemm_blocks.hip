@@ -360,7 +360,7 @@ using Tile64 = BlockTile<1, 4, 4, 1, 3, 3>;    // 64 x 64, a wave 64 x 16
 template <class T, int ACT>
 hipError_t launch_tile(const GemmBlocksArgs& a, hipStream_t s) {
     const int64_t tiles_m = (a.m + T::BM - 1) / T::BM, tiles_n = (a.n + T::BN - 1) / T::BN;
-    if (tiles_m * tiles_n >= kMaxWorkgroups / 2) return hipErrorInvalidValue;
+    if (tiles_m * tiles_n * T::NT >= int64_t(1) << 32) return hipErrorInvalidValue;     // threads of a grid's dimension
     const dim3 grid(static_cast<unsigned>(tiles_m * tiles_n), static_cast<unsigned>(a.parts));
     gemm_blocks_kernel<T, ACT><<<grid, T::NT, 0, s>>>(a, static_cast<int>(tiles_m), static_cast<int>(tiles_n));
     return hipGetLastError();

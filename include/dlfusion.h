@@ -442,7 +442,7 @@ typedef struct {
  * inputs' type, may be x or residual itself, with its stride: a residual stream is
  * updated in place.  Any other overlap of the tensors' ranges, from first element
  * to last: DLF_ERR_ALIAS.  UNSUPPORTED: another type, cols above 2^23, 2^31 or more
- * rows, strides above 2^31, a scale_stride that is no multiple of 4. */
+ * rows, strides above 2^31, a scale_stride that is no multiple of 4 or above 2^20. */
 dlf_status dlf_rms_norm(const dlf_rms_norm_desc *d, const void *x, const void *residual,
                         const float *weight, void *sum, void *y, float *y_scale, void *stream);
 
@@ -497,7 +497,7 @@ dlf_status dlf_gemm_blocks_workspace_bytes(const dlf_gemm_blocks_desc *d, size_t
  *                may be NULL where that size is 0.  Scratch: calls that share one on
  *                overlapping streams race
  * UNSUPPORTED: k % 16 != 0, n or k above 2^23, m above 2^24, a scale stride that
- * is no multiple of 4, m * n of 2^38 or more. */
+ * is no multiple of 4 or above 2^20, m * n of 2^37 or more. */
 dlf_status dlf_gemm_blocks(const dlf_gemm_blocks_desc *d, const void *a, const float *a_scale,
                            const void *b, const float *b_scale, const float *col_shift,
                            const void *residual, void *c, void *workspace,

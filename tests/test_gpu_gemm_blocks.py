@@ -233,6 +233,30 @@ def test_scale_strides(m):
     check(make(m, 300, 1000 // 16 * 16, more=(12, 4)))
 
 
+@pytest.mark.parametrize("m", [20, 64, 130, 600])
+def test_largest_scale_strides(m):
+    check(make(m, 300, 400, more=((1 << 20) - 4, (1 << 20) - 4)))
+
+
+def test_tensors_off_the_current_device_are_refused():
+    import dl_fusion_amd as dl
+    s = make(4, 256, 512)
+    d = dl.gemm_blocks_desc(4, 256, 512)
+    c = torch.empty(4, 256, dtype=torch.bfloat16, device="cuda")
+    rows, norm, quant = torch.zeros(4, 512, device="cuda"), dl.rms_norm_desc(4, 512, dtype="f32", out_dtype="f32"), dl.quant_blocks_desc(4, 512, "f32")
+    for off in ("a", "c"):
+        a, out = (s["a"].cpu(), c) if off == "a" else (s["a"], c.cpu())
+        with pytest.raises(ValueError):
+            dl.dlf_gemm_blocks(d, a, s["a_scale"], s["b"], s["b_scale"], None, None, out, None, 0)
+        with pytest.raises(ValueError):
+            dl.dlf_gemm_blocks_gated(d, a, s["a_scale"], s["b"], s["b_scale"], None, "silu", out[:, :128].contiguous(), None, 0)
+        x, y = (rows.cpu(), rows) if off == "a" else (rows, rows.cpu())
+        with pytest.raises(ValueError):
+            dl.dlf_rms_norm(norm, x, None, None, None, y, None)
+        with pytest.raises(ValueError):
+            dl.dlf_quant_blocks(quant, x, torch.empty(4, 512, dtype=FP8, device=y.device), s["a_scale"])
+
+
 @pytest.mark.parametrize("m", [3, 60, 140, 600])
 def test_each_block_has_its_own_scale(m):
     """One value a block, powers of two: the result is exact, and names every scale that it used."""

@@ -44,6 +44,7 @@ def call_norm(x=addr(0), residual=addr(1), weight=addr(2), sum=addr(3), y=addr(4
     (dict(out_dtype="fp8", out_inv_scale=INF), INVALID), (dict(y_scale=addr(5)), INVALID),
     (dict(y_scale=addr(5), out_dtype="fp8", y_scale_stride=1), INVALID),
     (dict(y_scale=addr(5), out_dtype="fp8", y_scale_stride=6), UNSUPPORTED),
+    (dict(y_scale=addr(5), out_dtype="fp8", y_scale_stride=(1 << 20) + 4), UNSUPPORTED),
 ])
 def test_norm_refuses_bad_descriptors(kw, status):
     assert call_norm(**kw) == status
@@ -114,7 +115,7 @@ def test_quant_refusals():
                dict(x=None), dict(codes=None), dict(scale=None), dict(x=addr(9, 2)), dict(codes=addr(9, 8)), dict(scale=addr(9, 4))):
         assert call_quant(**kw) == INVALID, kw
     for kw in (dict(dtype="fp8"), dict(cols=(1 << 23) + 1), dict(rows=1 << 31), dict(x_stride=(1 << 31) + 8),
-               dict(row_scale_stride=7), dict(rows=1 << 28, cols=1024)):
+               dict(row_scale_stride=7), dict(row_scale_stride=(1 << 20) + 4), dict(rows=1 << 28, cols=1024)):
         assert call_quant(**kw) == UNSUPPORTED, kw
     assert call_quant(rows=0, x=None, codes=None, scale=None) == OK
     assert call_quant(codes=addr(0, 2032)) == ALIAS
@@ -152,8 +153,9 @@ BAD_GEMMS = [
     (dict(m=-1), INVALID), (dict(n=-2), INVALID), (dict(k=-16), INVALID), (dict(act=4), INVALID),
     (dict(act=-1), INVALID), (dict(k=520), UNSUPPORTED), (dict(k=8), UNSUPPORTED),
     (dict(n=(1 << 23) + 2), UNSUPPORTED), (dict(k=(1 << 23) + 16), UNSUPPORTED), (dict(m=(1 << 24) + 1), UNSUPPORTED),
-    (dict(m=1 << 20, n=1 << 18), UNSUPPORTED), (dict(a_scale_stride=3), INVALID), (dict(b_scale_stride=0), INVALID),
+    (dict(m=1 << 20, n=1 << 17), UNSUPPORTED), (dict(a_scale_stride=3), INVALID), (dict(b_scale_stride=0), INVALID),
     (dict(a_scale_stride=5), UNSUPPORTED), (dict(b_scale_stride=6), UNSUPPORTED),
+    (dict(a_scale_stride=(1 << 20) + 4), UNSUPPORTED), (dict(b_scale_stride=(1 << 20) + 4), UNSUPPORTED),
 ]
 
 
@@ -196,7 +198,7 @@ def test_workspace_sizes(m):
     """Whole fp32 outputs, rows rounded up to 4 columns, at most 8 of them; none where nothing is summed."""
     for n in (0, 1, 2, 5, 64, 300, 1024, 4096, 22016):
         for k in (0, 16, 128, 1024, 4096, 11008, 1 << 23):
-            if m * n >= 1 << 38:
+            if m * n >= 1 << 37:
                 continue
             size = dlf.dlf_gemm_blocks_workspace_bytes(dlf.gemm_blocks_desc(m, n, k))
             one = m * (-(-n // 4) * 4) * 4
