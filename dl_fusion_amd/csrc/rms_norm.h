@@ -7,6 +7,11 @@
 // or the launch where there are few rows.  A thread holds 8 neighbouring columns at a time, so that a row
 // is read in whole lines and 16 neighbouring lanes hold a block of 128 columns: its largest magnitude is a
 // maximum over those lanes, no LDS.
+//
+// On the device, from a graph: 8192 rows of 4096 bf16 columns with residual and sum into codes 42 us (5.6 TB/s; a copy
+// reaches 5.2), 64 rows 3.3 us, one row into bf16 2.6 us, against 2.2 us of an empty kernel; the quantiser 8192 rows of 4096
+// columns 20 us (5.0 TB/s), 64 rows 2.3.  Rows that do not start at 16 bytes cost up to a quarter more (8192 x 4096, us: stride
+// 4096 | 4097, bf16 output 45.8 | 55.2, codes 41.8 | 48.3; 4095 columns close together 57.4 and 51.2; fp32 rows nothing).
 #pragma once
 
 #include "block_scale.h"
@@ -34,32 +39,56 @@ __device__ __forceinline__ void put(V* p, V v) {
     else *p = v;
 }
 
-template <bool STREAM>
-__device__ __forceinline__ void load8(const uint16_t* p, float* v) {
-    const u32x4_t x = get<STREAM>(reinterpret_cast<const u32x4_any_t*>(p));
+// 8 values as they lie in memory: loaded and looked at in two steps, so that the loads of all tensors are on their way together.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<uint16_t> {
+    u32x4_t x;
+    template <bool STREAM>
+    __device__ __forceinline__ void load(const uint16_t* p) { x = get<STREAM>(reinterpret_cast<const u32x4_any_t*>(p)); }
+    __device__ __forceinline__ void to(float* v) const {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(x[i] << 16);
-        v[2 * i + 1] = __uint_as_float(x[i] & 0xFFFF0000u);
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(x[i] << 16);
+            v[2 * i + 1] = __uint_as_float(x[i] & 0xFFFF0000u);
+        }
     }
-}
-template <bool STREAM>
-__device__ __forceinline__ void load8(const float* p, float* v) {
-    const f32x4_t a = get<STREAM>(reinterpret_cast<const f32x4_any_t*>(p)), b = get<STREAM>(reinterpret_cast<const f32x4_any_t*>(p + 4));
+};
+template <>
+struct Raw8<float> {
+    f32x4_t a, b;
+    template <bool STREAM>
+    __device__ __forceinline__ void load(const float* p) {
+        a = get<STREAM>(reinterpret_cast<const f32x4_any_t*>(p));
+        b = get<STREAM>(reinterpret_cast<const f32x4_any_t*>(p + 4));
+    }
+    __device__ __forceinline__ void to(float* v) const {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) { v[i] = a[i]; v[4 + i] = b[i]; }
-}
+        for (int i = 0; i < 4; ++i) { v[i] = a[i]; v[4 + i] = b[i]; }
+    }
+};
 __device__ __forceinline__ float load1(const uint16_t* p) { return bf16_to_f32(*p); }
 __device__ __forceinline__ float load1(const float* p) { return *p; }
 
-// 8 values, or n of a row's end and zeros behind them
+// Columns at .. at + 7 of a row, zeros behind its end.  What reaches past the end is loaded as the row's last 8 values and moved
+// down in registers (end_chunk), so that no load stands behind a branch (8192 rows of 4095 columns, us: value by value 75,
+// so 51).  Rows of less than 8 columns are SHORT, and loaded value by value.  A chunk that begins past the end is zeros.
 template <bool STREAM, typename T>
-__device__ __forceinline__ void load_chunk(const T* p, int n, float* v) {
-    if (n >= 8) {
-        load8<STREAM>(p, v);
-    } else {
+__device__ __forceinline__ Raw8<T> load_chunk(const T* row, int at, int cols) {
+    Raw8<T> r;
+    r.template load<STREAM>(row + (at + 8 <= cols ? at : cols - 8));
+    return r;
+}
+__device__ __forceinline__ void end_chunk(int at, int cols, float* v) {
+    const int back = at + 8 - cols;
+    if (back > 0) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = i < n ? load1(p + i) : 0.0f;
+        for (int d = 1; d < 8; d *= 2)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = back & d ? (i + d < 8 ? v[i + d] : 0.0f) : v[i];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = back < 8 ? v[i] : 0.0f;
     }
 }
 
@@ -117,29 +146,45 @@ __device__ __forceinline__ void store_block(const float* v, int n, int lane, uin
 // A row per group of TPR threads, V chunks of 8 columns a thread in registers; V = 0: rows beyond that, read
 // again from memory for the second pass.  Each element is read by the thread that writes it, and written after
 // both passes have read it or in place of it: sum and y may be an input itself.
-template <typename T, int OUT, int TPR, int V, bool STREAM>
-__global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void rms_norm_kernel(const RmsNormArgs p) {
+template <typename T, int OUT, int TPR, int V, bool STREAM, bool SHORT = false>
+__global__ __launch_bounds__(TPR == 64 ? 256 : TPR, V == 1 ? 8 : 4) void rms_norm_kernel(const RmsNormArgs p) {
     constexpr int kRows = TPR == 64 ? 4 : 1;        // a workgroup has several rows only where a row is a wave's: no barrier
     constexpr int kWaves = TPR / 64;
     __shared__ float part[kWaves];
-    const int tid = static_cast<int>(threadIdx.x) % TPR, lane = tid & 63;
+    const int tid = kRows > 1 ? static_cast<int>(threadIdx.x) % TPR : static_cast<int>(threadIdx.x), lane = tid & 63;
     const int cols = p.cols;
     const float* const w = p.weight;
     // every thread of a workgroup takes as many turns: the barriers below are met by all
     for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * kRows; row0 < p.rows; row0 += static_cast<int64_t>(gridDim.x) * kRows) {
-        const int64_t row = row0 + static_cast<int>(threadIdx.x) / TPR;
+        const int64_t row = kRows > 1 ? row0 + __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / TPR) : row0;  // uniform
         if (kRows > 1 && row >= p.rows) return;
         const T* const x = static_cast<const T*>(p.x) + row * p.x_stride;
         const T* const res = p.residual ? static_cast<const T*>(p.residual) + row * p.residual_stride : nullptr;
         T* const sum = p.sum ? static_cast<T*>(p.sum) + row * p.sum_stride : nullptr;
         auto load_h = [&](int at, float* h) __attribute__((always_inline)) {
-            load_chunk<STREAM>(x + at, cols - at, h);
+            if constexpr (SHORT) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    h[i] = load1(x + (i < cols ? i : 0));
+                    if (res) h[i] += load1(res + (i < cols ? i : 0));
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) h[i] = at + i < cols ? h[i] : 0.0f;
+                return;
+            }
+            const Raw8<T> a = load_chunk<STREAM>(x, at, cols);
+            Raw8<T> b;
+            if (res) b = load_chunk<STREAM>(res, at, cols);
+            // both on their way before the first is waited for (8192 rows of 4096 columns, us: 45.7 | 41.8)
+            __builtin_amdgcn_sched_barrier(0);
+            a.to(h);
             if (res) {
                 float r[8];
-                load_chunk<STREAM>(res + at, cols - at, r);
+                b.to(r);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) h[i] += r[i];
             }
+            end_chunk(at, cols, h);
         };
         auto all_sum = [&](float s) __attribute__((always_inline)) {
 #pragma unroll
@@ -154,6 +199,10 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void rms_norm_kernel(const R
             }
             return s;
         };
+        // The weights of a single chunk come with the row, and not behind its sum.  (Those of two would take 88 registers instead of
+        // 66, and waves with them: 4096 rows of 8192 columns, us: 53.4 | 48.1.)
+        constexpr bool kEarly = V == 1 && !SHORT;
+        Raw8<float> early[kEarly ? V : 1];
         float h[V > 0 ? V : 1][8];
         auto squares = [&](float factor) __attribute__((always_inline)) {
             float s = 0.0f;
@@ -179,9 +228,8 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void rms_norm_kernel(const R
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const int at = 8 * (tid + j * TPR);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) h[j][i] = 0.0f;
-                if (at < cols) load_h(at, h[j]);
+                if (kEarly && w) early[kEarly ? j : 0] = load_chunk<false>(w, at, cols);
+                load_h(at, h[j]);
             }
         }
         float total = squares(1.0f);
@@ -194,14 +242,21 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void rms_norm_kernel(const R
             total = squares(factor);
         }
         const float r = 1.0f / sqrtf(total / static_cast<float>(cols) + eps);
-        auto finish = [&](int at, const float* v) __attribute__((always_inline)) {
+        auto finish = [&](int at, int j, const float* v) __attribute__((always_inline)) {
             const int n = cols - at;
             float y[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) y[i] = v[i] * factor * r;
-            if (w && n > 0) {
+            if (w) {
                 float f[8];
-                load_chunk<false>(w + at, n, f);
+                if constexpr (SHORT) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) f[i] = i < n ? load1(w + i) : 0.0f;
+                } else {
+                    if constexpr (kEarly) early[j].to(f);
+                    else load_chunk<false>(w, at, cols).to(f);
+                    end_chunk(at, cols, f);
+                }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) y[i] *= f[i];
             }
@@ -221,15 +276,13 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void rms_norm_kernel(const R
         };
         if constexpr (V > 0) {
 #pragma unroll
-            for (int j = 0; j < V; ++j) finish(8 * (tid + j * TPR), h[j]);
+            for (int j = 0; j < V; ++j) finish(8 * (tid + j * TPR), j, h[j]);
         } else {
             // all lanes of a block's 16 go together
             for (int base = 0; base < cols; base += 8 * TPR) {
                 const int at = base + 8 * tid;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) h[0][i] = 0.0f;
-                if (at < cols) load_h(at, h[0]);
-                finish(at, h[0]);
+                load_h(at, h[0]);
+                finish(at, 0, h[0]);
             }
         }
     }
@@ -237,27 +290,34 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void rms_norm_kernel(const R
 
 // 16 lanes a block of 128 columns, blocks numbered row by row; U of them a thread, whose loads are all on their way
 // before the first is used.
-template <typename T, int U, bool STREAM>
+template <typename T, int U, bool STREAM, bool SHORT = false>
 __global__ __launch_bounds__(256) void quant_blocks_kernel(const QuantBlocksArgs p) {
     const int lane = static_cast<int>(threadIdx.x) & 15;
     for (uint32_t first = blockIdx.x * (16 * U) + threadIdx.x / 16; first < p.blocks; first += gridDim.x * (16 * U)) {
-        float v[U][8];
+        Raw8<T> raw[U];
         uint32_t row[U], b[U];
         int at[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const uint32_t block = first + 16 * u;
+            const uint32_t block = first + 16 * u < p.blocks ? first + 16 * u : first;     // the first again: as it is
             row[u] = block / static_cast<uint32_t>(p.row_blocks);
             b[u] = block - row[u] * static_cast<uint32_t>(p.row_blocks);
-            at[u] = block < p.blocks ? static_cast<int>(b[u]) * kScaleBlock + 8 * lane : p.cols;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[u][i] = 0.0f;
-            if (at[u] < p.cols) load_chunk<STREAM>(static_cast<const T*>(p.x) + row[u] * p.x_stride + at[u], p.cols - at[u], v[u]);
+            at[u] = static_cast<int>(b[u]) * kScaleBlock + 8 * lane;
+            if constexpr (!SHORT) raw[u] = load_chunk<STREAM>(static_cast<const T*>(p.x) + row[u] * p.x_stride, at[u], p.cols);
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            store_block<STREAM>(v[u], p.cols - at[u], lane, p.codes + row[u] * p.codes_stride + at[u],
+        for (int u = 0; u < U; ++u) {
+            float v[8];
+            if constexpr (SHORT) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = at[u] + i < p.cols ? load1(static_cast<const T*>(p.x) + row[u] * p.x_stride + i) : 0.0f;
+            } else {
+                raw[u].to(v);
+                end_chunk(at[u], p.cols, v);
+            }
+            store_block<STREAM>(v, p.cols - at[u], lane, p.codes + row[u] * p.codes_stride + at[u],
                                 p.scale + static_cast<int64_t>(row[u]) * p.scale_stride + b[u]);
+        }
     }
 }
 
@@ -279,6 +339,7 @@ hipError_t launch(const RmsNormArgs& a, hipStream_t s) {
         kernel<<<groups < kMostGroups ? static_cast<unsigned>(groups) : kMostGroups, tpr == 64 ? 256 : tpr, 0, s>>>(a);
         return hipGetLastError();
     };
+    if (a.cols < 8) return go(rms_norm_kernel<T, OUT, 64, 1, STREAM, true>, 64);
     if (a.cols <= 512) return go(rms_norm_kernel<T, OUT, 64, 1, STREAM>, 64);
     if (a.cols <= 1024) return go(rms_norm_kernel<T, OUT, 128, 1, STREAM>, 128);
     if (a.cols <= 2048) return go(rms_norm_kernel<T, OUT, 256, 1, STREAM>, 256);
@@ -305,10 +366,11 @@ hipError_t launch_out(const RmsNormArgs& a, int out, hipStream_t s) {
 
 template <typename T>
 hipError_t launch_quant(const QuantBlocksArgs& a, hipStream_t s) {
-    const bool stream = static_cast<int64_t>(a.blocks) * kScaleBlock * (sizeof(T) + 1) >= kStreamBytes;
+    const bool stream = a.cols >= 8 && static_cast<int64_t>(a.blocks) * kScaleBlock * (sizeof(T) + 1) >= kStreamBytes;
     // two blocks a thread cost 0.5 us where there are few, and gain 4% where there are many
     const unsigned each = stream ? 32 : 16, all = (a.blocks + each - 1) / each, groups = all < kMostGroups ? all : kMostGroups;
-    if (stream) quant_blocks_kernel<T, 2, true><<<groups, 256, 0, s>>>(a);
+    if (a.cols < 8) quant_blocks_kernel<T, 1, false, true><<<groups, 256, 0, s>>>(a);
+    else if (stream) quant_blocks_kernel<T, 2, true><<<groups, 256, 0, s>>>(a);
     else quant_blocks_kernel<T, 1, false><<<groups, 256, 0, s>>>(a);
     return hipGetLastError();
 }

@@ -437,8 +437,8 @@ typedef struct {
  *   sum       device [rows][cols] of d->dtype, or NULL (not stored)
  *   y         device [rows][cols] of d->out_dtype
  *   y_scale   device [rows][scale_stride] fp32, or NULL; FP8_E4M3 only
- * Rows may start at any element (odd widths and strides cost 10 to 40%, see the
- * kernel); the tensors themselves are 16-byte aligned.  sum, and y where it has the
+ * Rows may start at any element (those that do not start at 16 bytes take up to a
+ * quarter longer); the tensors themselves are 16-byte aligned.  sum, and y where it has the
  * inputs' type, may be x or residual itself, with its stride: a residual stream is
  * updated in place.  Any other overlap of the tensors' ranges, from first element
  * to last: DLF_ERR_ALIAS.  UNSUPPORTED: another type, cols above 2^23, 2^31 or more
@@ -486,7 +486,7 @@ dlf_status dlf_gemm_blocks_workspace_bytes(const dlf_gemm_blocks_desc *d, size_t
  * cores cut each product of two codes 2^-14 below the largest of its neighbours
  * (measured: 2e-6 of sum |a b| on normal values, against the 2^-9 of c's own rounding).
  * The order of the sums depends on the descriptor alone: the same inputs give the
- * same bits.
+ * same bits.  The product of two scales is taken in fp32 first: it has to be in range.
  *   a, a_scale   device e4m3 [m][k] and fp32 [m][a_scale_stride]
  *   b, b_scale   device e4m3 [n][k] and fp32 [ceil(n / 128)][b_scale_stride]
  *   col_shift    device [n] fp32 or NULL (= 0)

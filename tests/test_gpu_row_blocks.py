@@ -179,7 +179,7 @@ def test_norm_of_more_rows_than_a_launch_has_workgroups_for():
     assert ((y - want).abs() <= 50 * U * want.abs()).all()
 
 
-@pytest.mark.parametrize("cols", [96, 4096, 20000])
+@pytest.mark.parametrize("cols", [5, 13, 96, 1003, 4096, 4099, 12301, 20000, 20003])
 @pytest.mark.parametrize("where", ["sum is x", "sum is residual", "y is x", "y is residual", "y is x, sum is residual"])
 def test_norm_in_place(cols, where):
     import dl_fusion_amd as dl
