@@ -1,4 +1,16 @@
 // Products with block scales: tiles of 64 x 64 to 256 x 256 outputs a workgroup, and the choice among the kernels.
+//
+// A wave's fragments of b stay in registers for a block of k, those of a pass by, one for each FN MFMAs; each MFMA's result is a
+// block's whole sum, which the vector ALU scales and adds while the matrix cores do the next.  That keeps the sums in VGPRs
+// (the vector ALU reads no AGPRs), and FN x FM fragments of 4 with the operands' rings are what 256 registers hold: 128 x 64
+// a wave, eight waves a CU for 256 x 256 outputs.
+//
+// What bounds: many rows, the bytes into each CU.  8192 x 22016 x 4096 gated takes 615 us (2.4 PFLOP/s), 8192 x 4096 x 11008 295
+// (2.5): the matrix cores are busy 62 to 66% of the clocks at 1.7 to 1.8 GHz; a block's 64 KB come from L2 (80% hits) 330 to 355
+// clocks after they are asked for, at 37 KB a us and CU; without the loads (a timing copy) the cores are busy 80%.
+// The scaling costs 3.5% (against plain sums).  Smaller tiles take more bytes an output: 777 x 5000 x 4112 33 us in tiles of
+// 128 x 128, of which 303 MB into the CUs are 27.  Few rows, the read of b: 64 x 22016 x 4096 gated 18.2 us on the device
+// (5.0 TB/s of b), 64 x 4096 x 11008 14 us in parts of the sum (3.3 TB/s) and 3.9 for their join.
 #include "gemm_blocks.h"
 
 namespace dlf {
@@ -28,8 +40,9 @@ struct BlockTile {
     static_assert(BM % 64 == 0 && (BN == 128 || BN == 256 || BN == 64), "scales of whole waves, at most two rows of b's");
 };
 
-// Tile of a linear workgroup number: see tile_coords of the other products.  Neighbouring numbers are dealt to the 8 XCDs
-// in turn; each gets a contiguous range, in groups of G tile rows that sweep the columns.
+// Tile of a linear workgroup number.  Neighbouring numbers are dealt to the 8 XCDs in turn; each XCD gets a contiguous range, in
+// groups of G tile rows that sweep the columns, so that the 32 tiles that run on it share panels in its L2.  (G = 4 and 16
+// were not faster than 8.)
 template <int G>
 __device__ __forceinline__ void xcd_tile(int tiles_m, int tiles_n, int bid, int& tm, int& tn) {
     const int nb = tiles_m * tiles_n, xcd = bid & 7, local = bid >> 3, q = nb >> 3, r = nb & 7;

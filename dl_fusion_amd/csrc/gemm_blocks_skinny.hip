@@ -4,10 +4,11 @@
 namespace dlf {
 namespace {
 
-// Few rows of a: what bounds is the read of b, once.  A wave has a ring of DEPTH stages of its own, of one block of k
-// each, for 16 R rows of b and all 16 TM rows of a, and takes every NW-th block; no wave waits for another until
-// their sums are added through LDS at the end.  With blockIdx.y the blocks are cut once more, and the parts go to the
-// workspace as they are.
+// Few rows of a: what bounds is the read of b, once: one row through 4096 x 4096 takes 4.7 us on the device (16.8 MB: 3.2 us at
+// a copy's 5.2 TB/s, and 2.2 of an empty launch), through 22016 x 4096 18.5 as called (4.9 TB/s).  A wave has a ring of DEPTH
+// stages of its own, of one block of k each, for 16 R rows of b and all 16 TM rows of a, and takes every NW-th block; no wave
+// waits for another until their sums are added through LDS at the end.  With blockIdx.y the blocks are cut once more, and
+// the parts go to the workspace as they are.
 template <int TM, int R, int NW, int DEPTH>
 struct Skinny {
     static constexpr int kLoads = 2 * R + 2 * TM + 1;           // of a wave and stage: b, a, and a's scales
@@ -44,7 +45,7 @@ __global__ __launch_bounds__(64 * NW, 2) void gemm_blocks_skinny_kernel(const Ge
     typedef const __attribute__((address_space(4))) float* scalar_t;
     const int slab = GATED ? 2 * (n0 / (2 * kScaleBlock)) : n0 / kScaleBlock;
     const scalar_t sb0 = (scalar_t)(p.b_scale + static_cast<int64_t>(slab) * p.b_scale_stride), sb1 = GATED ? sb0 + p.b_scale_stride : sb0;
-    // Loads as in the tiles above: 8 rows of whole lines each, chunk c of row r at c ^ (r / 2 % 8).  Load l holds rows
+    // Loads as those of the tiles: 8 rows of whole lines each, chunk c of row r at c ^ (r / 2 % 8).  Load l holds rows
     // 8 l .., so that the order of its chunks depends on l's parity.
     const int chunk = (lane & 7) ^ (lane >> 4);
     const uint32_t from = static_cast<uint32_t>(lane >> 3) * static_cast<uint32_t>(k);
