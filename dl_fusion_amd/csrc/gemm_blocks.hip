@@ -156,12 +156,17 @@ __global__ __launch_bounds__(T::NT, T::kWaves) void gemm_blocks_kernel(const Gem
     // of the waves' rows of a with group kHalf, when all have read them, the second halves DEPTH groups before the end; the loads
     // of the block that is to lie there follow as evenly as the MFMAs, kEach a group, so that they find no queue and each has more
     // than a block's time, and the same two barriers say that the loads that are read next have landed.  With few groups a second
-    // barrier costs more than it gives: all comes free DEPTH groups before the end, half of the loads follow at once, half in the
-    // next block's first group.  (us, one step | two, with inputs that no cache holds: 8192 x 22016 x 4096 gated 651 | 627,
-    // 8192 x 4096 x 11008 316 | 299; 777 x 5000 x 4112, four groups, 34.3 | 38.5.)
+    // barrier costs more than it gives: all comes free DEPTH groups before the end.  In a ring of three all loads follow at once;
+    // in a ring of two half of them do and half in the next block's first group, which is faster where two workgroups share a CU.
+    // (us, one step | two, with inputs that no cache holds: 8192 x 22016 x 4096 gated 651 | 627, 8192 x 4096 x 11008 316 | 299;
+    // 777 x 5000 x 4112, four groups, 34.3 | 38.5.  Four groups, a ring of two, half of the loads later | none: 777 x 5000 x 4112
+    // 33.3 | 35.1, 640 x 8192 x 2048 18.9 | 19.4.)
     constexpr int DEPTH = 2, RING = 4;      // fragments of a are read DEPTH groups of MFMAs ahead
     constexpr bool kTwice = FM >= 8;
     constexpr int kHalf = FM / 2 - 2, kEach = kLoads / FM;
+    constexpr bool kOnce = T::STAGES > 2;
+    constexpr int kNow = kOnce ? kLoads : kLoads / 2;       // of the loads in one step, those that follow at once
+    static_assert(!kTwice || T::STAGES == 2, "a ring of two stages frees in two steps");
     if (blocks > 0) {
         fetch_scales(0);
 #pragma unroll
@@ -173,7 +178,7 @@ __global__ __launch_bounds__(T::NT, T::kWaves) void gemm_blocks_kernel(const Gem
         wait_vmcnt<(T::STAGES - 2) * kLoads>();
         barrier();
 #pragma unroll
-        for (int q = 0; q < (kTwice ? kLoads - kHalf * kEach : kLoads / 2); ++q) load_part((T::STAGES - 1) * T::kStage, q, load_off(T::STAGES - 1));
+        for (int q = 0; q < (kTwice ? kLoads - kHalf * kEach : kNow); ++q) load_part((T::STAGES - 1) * T::kStage, q, load_off(T::STAGES - 1));
         i32x8_t w[FN], x[RING];
         f32x4_t sa[T::H];                   // scales of the rows of four fragments
         float b0, b1;                       // of the wave's columns, even and odd
@@ -228,10 +233,10 @@ __global__ __launch_bounds__(T::NT, T::kWaves) void gemm_blocks_kernel(const Gem
                         }
                     } else if (i >= FM - DEPTH) {
 #pragma unroll
-                        for (int q = 0; q < kLoads / 4; ++q) load_part(stage, (i - FM + DEPTH) * (kLoads / 4) + q, off);
+                        for (int q = 0; q < kNow / 2; ++q) load_part(stage, (i - FM + DEPTH) * (kNow / 2) + q, off);
                     } else if (i == 0) {
 #pragma unroll
-                        for (int q = kLoads / 2; q < kLoads; ++q) load_part(last, q, off_last);
+                        for (int q = kNow; q < kLoads; ++q) load_part(last, q, off_last);
                     }
                     const float t0 = s0, t1 = s1;
                     s0 = sa[i >> 2][i & 3] * b0;
@@ -259,8 +264,8 @@ __global__ __launch_bounds__(T::NT, T::kWaves) void gemm_blocks_kernel(const Gem
 #pragma unroll
                     for (int j = 0; j < FN; ++j) {
                         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                        if (kTwice ? j < kEach : j % 2 == 0 && (i == 0 || i >= FM - DEPTH))
-                            __builtin_amdgcn_sched_group_barrier(0x020, kTwice || kLoads < 8 ? 1 : kLoads / 8, 0);
+                        if (kTwice ? j < kEach : kOnce ? i >= FM - DEPTH : j % 2 == 0 && (i == 0 || i >= FM - DEPTH))
+                            __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
                         if (i + 1 == FM) __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
                         else __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
                         __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);
@@ -367,7 +372,10 @@ __global__ __launch_bounds__(T::NT, T::kWaves) void gemm_blocks_kernel(const Gem
 }
 
 using Tile256 = BlockTile<2, 4, 8, 4>;      // 256 x 256, a wave 128 x 64
-using Tile128 = BlockTile<2, 2, 4, 4>;      // 128 x 128, a wave 64 x 64
+using Tile128 = BlockTile<2, 2, 4, 4>;      // 128 x 128, a wave 64 x 64; two workgroups a CU
+// The same alone on its CU, where there are no more than CUs (us, two stages | three: 1024 x 4096 x 4096 30.3 | 26.5, 512 x 5000 x
+// 4112 30.1 | 26.1).
+using Tile128Deep = BlockTile<2, 2, 4, 4, 3, 1>;
 using Tile64 = BlockTile<1, 4, 4, 1, 3, 3>;    // 64 x 64, a wave 64 x 16
 
 template <class T, int ACT>
@@ -384,21 +392,23 @@ hipError_t launch(const GemmBlocksArgs& a, hipStream_t s) {
     switch (a.kind) {
         case kGemmBlocksTile64: return launch_tile<Tile64, ACT>(a, s);
         case kGemmBlocksTile128: return launch_tile<Tile128, ACT>(a, s);
+        case kGemmBlocksTile128Deep: return launch_tile<Tile128Deep, ACT>(a, s);
         default: return launch_tile<Tile256, ACT>(a, s);
     }
 }
 
 // What a tile takes, in us: `more`, and for each block of k slope + share w + chip f, w workgroups on its CU and a share f of all
-// places of the chip taken.  Fitted to 180 sizes of 33 to 8192 rows, 300 to 22016 columns and sums of 1024 to 11008, each
-// measured with every tile and number of parts; the choice by it is 0.4% slower than the best on average, 16% at worst.
+// places of the chip taken.  Fitted to 224 sizes of 33 to 8192 rows, 300 to 22016 columns and sums of 1024 to 11008, each
+// measured with every tile and number of parts; the choice by it is 0.6% slower than the best on average, 11% at worst.
 struct TileCost {
     int kind, rows, cols, on_a_cu;
     double slope, share, chip, more;
 };
 constexpr TileCost kCosts[] = {
-    {kGemmBlocksTile64, 64, 64, 3, 0.13, 0.16, 0.0, 1.0},
-    {kGemmBlocksTile128, 128, 128, 2, 0.38, 0.32, 0.0, 1.2},
-    {kGemmBlocksTile256, 256, 256, 1, 1.2, 0.0, 0.35, 4.0},
+    {kGemmBlocksTile64, 64, 64, 3, 0.13, 0.15, 0.0, 0.8},
+    {kGemmBlocksTile128, 128, 128, 2, 0.34, 0.28, 0.0, 0.8},
+    {kGemmBlocksTile128Deep, 128, 128, 1, 0.48, 0.0, 0.1, 1.2},
+    {kGemmBlocksTile256, 256, 256, 1, 0.66, 0.0, 0.64, 2.7},
 };
 
 }  // namespace
@@ -447,7 +457,7 @@ void plan_gemm_blocks(GemmBlocksArgs* a) {
             double us = static_cast<double>(full) * (blocks * (c.slope + c.share * c.on_a_cu + c.chip) + c.more);
             if (rest > 0)
                 us += blocks * (c.slope + c.share * static_cast<double>((rest + kCus - 1) / kCus) + c.chip * static_cast<double>(rest) / (kCus * c.on_a_cu)) + c.more;
-            if (parts > 1) us += 2.0 + parts * static_cast<double>(a->m) * a->n * 8 / 5.5e6;
+            if (parts > 1) us += 2.1 + parts * static_cast<double>(a->m) * a->n * 8 / 5e6;
             if (best == 0 || us < best) {
                 best = us;
                 a->kind = c.kind;

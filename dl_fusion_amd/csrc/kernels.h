@@ -292,7 +292,7 @@ struct GemmBlocksArgs {
 // the kernels: up to 16 or 32 rows of a, 16 rows of b a workgroup or 32, and tiles
 enum : int {
     kGemmBlocks16 = 0, kGemmBlocks16Wide = 1, kGemmBlocks32 = 2, kGemmBlocks32Wide = 3,
-    kGemmBlocksTile64 = 4, kGemmBlocksTile128 = 5, kGemmBlocksTile256 = 6
+    kGemmBlocksTile64 = 4, kGemmBlocksTile128 = 5, kGemmBlocksTile128Deep = 6, kGemmBlocksTile256 = 7
 };
 void plan_gemm_blocks(GemmBlocksArgs* args);    // fills kind, parts, part_blocks and part_stride from m, n and k
 // act: kAct*, or kActSiluMul.. for the gated form

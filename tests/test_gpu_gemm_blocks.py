@@ -170,6 +170,13 @@ def test_large(m, n, k, gate):
     check(make(m, n, k, gate is not None), gate=gate)
 
 
+@pytest.mark.parametrize("m,n,k,gate", [(1000, 4000, 2064, None), (900, 3900, 1424, "gelu_tanh"), (700, 5001, 4096, None),
+                                        (1024, 4096, 1536, "silu"), (520, 6100, 3000 // 16 * 16, None), (130, 15000, 1680, None),
+                                        (2000, 2050, 6000, "gelu_erf"), (385, 4098, 11008, None)])
+def test_about_as_many_tiles_as_cus(m, n, k, gate):
+    check(make(m, n, k, gate is not None, shift=True, residual=gate is None), gate=gate)
+
+
 @pytest.mark.parametrize("m", [1, 16, 17, 32])
 @pytest.mark.parametrize("n", [6144, 6146, 6161, 8200])
 def test_few_rows_and_many_columns(m, n):
