@@ -5,12 +5,12 @@
 // (the vector ALU reads no AGPRs), and FN x FM fragments of 4 with the operands' rings are what 256 registers hold: 128 x 64
 // a wave, eight waves a CU for 256 x 256 outputs.
 //
-// What bounds: many rows, the bytes into each CU.  8192 x 22016 x 4096 gated takes 615 us (2.4 PFLOP/s), 8192 x 4096 x 11008 295
-// (2.5): the matrix cores are busy 62 to 66% of the clocks at 1.7 to 1.8 GHz; a block's 64 KB come from L2 (80% hits) 330 to 355
+// What bounds: many rows, the bytes into each CU.  8192 x 22016 x 4096 gated takes 615 to 641 us (2.4 PFLOP/s), 8192 x 4096 x 11008
+// 295 to 309 (2.5): the matrix cores are busy 62 to 66% of the clocks at 1.7 to 1.8 GHz; a block's 64 KB come from L2 (80% hits) 330 to 355
 // clocks after they are asked for, at 37 KB a us and CU; without the loads (a timing copy) the cores are busy 80%.
 // The scaling costs 3.5% (against plain sums).  Smaller tiles take more bytes an output: 777 x 5000 x 4112 33 us in tiles of
 // 128 x 128, of which 303 MB into the CUs are 27.  Few rows, the read of b: 64 x 22016 x 4096 gated 18.2 us on the device
-// (5.0 TB/s of b), 64 x 4096 x 11008 14 us in parts of the sum (3.3 TB/s) and 3.9 for their join.
+// (5.0 TB/s of b), 64 x 4096 x 11008 14 us in four parts of the sum (3.3 TB/s) and 4 for their join.
 #include "gemm_blocks.h"
 
 namespace dlf {
