@@ -684,6 +684,27 @@ def dlf_quant_blocks_weights(w, gated=False):
     return codes, scale
 
 
+class Buffers(dict):
+    """Tensors by name that a block keeps between calls and drops for larger ones.  The allocator knows the stream they were
+    made on only, and would hand them out there again while kernels on another stream still use them: each call says that it
+    uses them on its stream, and they come free when what that stream has been given by then is done."""
+
+    def __init__(self, **tensors):
+        super().__init__(tensors)
+        self._told = set()
+
+    def used(self):
+        """The current stream uses all of them.  0.2 us where it has said so before."""
+        device = torch.cuda.current_device()
+        key = device, torch._C._cuda_getCurrentRawStream(device)        # default streams of all devices have one handle
+        if key not in self._told:
+            stream = torch.cuda.current_stream(device)
+            for t in self.values():
+                t.record_stream(stream)
+            self._told.add(key)
+        return self
+
+
 def dlf_clock_probe(workgroups, iters, stamps, stream=None):
     """Enqueue the shader-clock probe; stamps: a device int64 tensor of 4 * workgroups values."""
     _check(_lib.dlf_clock_probe(int(workgroups), int(iters), _dev(stamps), _stream(stream)), "dlf_clock_probe")

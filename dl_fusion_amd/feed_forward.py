@@ -16,7 +16,7 @@ from __future__ import annotations
 import numpy as np
 import torch
 
-from . import (dlf_gemm_blocks, dlf_gemm_blocks_gated, dlf_gemm_blocks_workspace_bytes, dlf_quant_blocks,
+from . import (Buffers, dlf_gemm_blocks, dlf_gemm_blocks_gated, dlf_gemm_blocks_workspace_bytes, dlf_quant_blocks,
                dlf_quant_blocks_weights, dlf_rms_norm, gemm_blocks_desc, quant_blocks_desc, rms_norm_desc, scale_stride)
 
 FP8 = torch.float8_e4m3fn
@@ -54,7 +54,8 @@ class GatedFeedForward:
     """``gate_up`` and ``down``: what pack_gate_up and pack return.  ``norm``: fp32 [d_model] or None (= 1).
     ``rows``: rows of a call that may be captured: their buffers are made here and stay where they are.  Calls of other
     lengths share one set of buffers, which grows to the longest, and are refused under capture.  A set is one call's at a
-    time: calls on streams that overlap need a block each (the weights may be the same tensors)."""
+    time: calls on streams that overlap need a block each (the weights may be the same tensors); calls on one stream after
+    another, each waiting for the last, may share one."""
 
     def __init__(self, gate_up, down, norm=None, eps=1e-5, gate="silu", rows=0):
         self.gate_up, self.down, self.norm, self.eps, self.gate = gate_up, down, norm, eps, gate
@@ -64,7 +65,8 @@ class GatedFeedForward:
         if norm is not None and (tuple(norm.shape) != (self.d_model,) or norm.dtype != torch.float32):
             raise ValueError(f"norm must be fp32 [{self.d_model}]")
         self.rows = rows
-        self._own = self._views(rows, self._allocate(rows)) if rows > 0 else None
+        self._own_room = self._allocate(rows) if rows > 0 else None
+        self._own = self._views(rows, self._own_room) if rows > 0 else None
         self._shared = None
 
     def _descs(self, m):
@@ -74,12 +76,12 @@ class GatedFeedForward:
         device = self.down[0].device
         f32 = dict(dtype=torch.float32, device=device)
         ws = max([ws] + [dlf_gemm_blocks_workspace_bytes(d) for d in self._descs(m)])
-        return dict(x=torch.empty(m, self.d_model, dtype=FP8, device=device),
-                    x_scale=torch.empty(m, scale_stride(self.d_model), **f32),
-                    h=torch.empty(m, self.d_ff, dtype=torch.bfloat16, device=device),
-                    q=torch.empty(m, self.d_ff, dtype=FP8, device=device),
-                    q_scale=torch.empty(m, scale_stride(self.d_ff), **f32),
-                    ws=torch.empty(ws, dtype=torch.uint8, device=device))
+        return Buffers(x=torch.empty(m, self.d_model, dtype=FP8, device=device),
+                       x_scale=torch.empty(m, scale_stride(self.d_model), **f32),
+                       h=torch.empty(m, self.d_ff, dtype=torch.bfloat16, device=device),
+                       q=torch.empty(m, self.d_ff, dtype=FP8, device=device),
+                       q_scale=torch.empty(m, scale_stride(self.d_ff), **f32),
+                       ws=torch.empty(ws, dtype=torch.uint8, device=device))
 
     def _views(self, m, room):
         got = {n: t if n == "ws" else t[:m] for n, t in room.items()}
@@ -90,6 +92,7 @@ class GatedFeedForward:
 
     def _buffers(self, m):
         if m == self.rows and self._own is not None:
+            self._own_room.used()
             return self._own
         if torch.cuda.is_current_stream_capturing():
             raise ValueError(f"only calls of `rows` = {self.rows} rows may be captured, got {m}")
@@ -98,7 +101,7 @@ class GatedFeedForward:
             most, ws = (0, 0) if self._shared is None else (self._shared["x"].shape[0], self._shared["ws"].numel())
             self._shared = None             # before the next is made
             self._shared = self._allocate(max(m, most), max(ws, need))
-        return self._views(m, self._shared)
+        return self._views(m, self._shared.used())
 
     def __call__(self, x, y):
         """y = x + the block of x, both bf16 [rows][d_model] and contiguous; y is not x."""
