@@ -20,7 +20,7 @@ from __future__ import annotations
 
 import torch
 
-from . import (dlf_gemm_fused, dlf_lora_add, dlf_lora_workspace_bytes, dlf_page_plan, dlf_paged_attention,
+from . import (Buffers, dlf_gemm_fused, dlf_lora_add, dlf_lora_workspace_bytes, dlf_page_plan, dlf_paged_attention,
                dlf_paged_attention_workspace_bytes, dlf_paged_store, dlf_rms_norm, gemm_desc, kv_cache_desc, lora_desc,
                page_plan_desc, paged_attn_desc, rms_norm_desc)
 
@@ -86,14 +86,16 @@ class PagedAttentionBlock:
         them; batches of prompts of any length share one set, which grows to the longest."""
         if m == self.requests:
             if self._step is None:
-                self._step = self._views(m, self._allocate(m))
+                self._step_room = self._allocate(m)
+                self._step = self._views(m, self._step_room)
+            self._step_room.used()
             return self._step
         if self._prompts is None or self._prompts["rows"].numel() < m or (
                 self.adapters is not None and self._prompts["lora_ws"].numel() < self._lora(m)[1]):
             most, ws = (0, 0) if self._prompts is None else (self._prompts[n].numel() for n in ("rows", "lora_ws"))
             self._prompts = None            # before the next is made
             self._prompts = self._allocate(max(m, most), ws)
-        return self._views(m, self._prompts)
+        return self._views(m, self._prompts.used())
 
     def _lora(self, m):
         count, rank, _ = self.adapters[0].shape
@@ -105,11 +107,11 @@ class PagedAttentionBlock:
         device = self.w_qkv.device
         if self.adapters is not None:
             lora_ws = max(lora_ws, self._lora(m)[1])
-        return dict(slots=torch.empty(m, dtype=torch.int64, device=device),
-                    rows=torch.empty(m, dtype=torch.int32, device=device),
-                    qkv=torch.empty(m, self.width, dtype=torch.bfloat16, device=device),
-                    normed=torch.empty(m if self.norm is not None else 0, self.hidden, dtype=torch.bfloat16, device=device),
-                    lora_ws=torch.empty(lora_ws, dtype=torch.uint8, device=device))
+        return Buffers(slots=torch.empty(m, dtype=torch.int64, device=device),
+                       rows=torch.empty(m, dtype=torch.int32, device=device),
+                       qkv=torch.empty(m, self.width, dtype=torch.bfloat16, device=device),
+                       normed=torch.empty(m if self.norm is not None else 0, self.hidden, dtype=torch.bfloat16, device=device),
+                       lora_ws=torch.empty(lora_ws, dtype=torch.uint8, device=device))
 
     def _views(self, m, room):
         got = dict(plan=page_plan_desc(self.requests, self.page_size, self.max_pages, m, self.free.numel()),

@@ -63,3 +63,31 @@ def test_feed_forward_buffers_of_its_own_are_recorded_too(streams):
     for streams.now in (4, 5):
         own = block._buffers(8)
     assert {4, 5} <= streams.on([own[n] for n in NAMES])
+
+
+def attention(requests=4):
+    from dl_fusion_amd.decode import PagedAttentionBlock
+    heads, kv, dim, hidden, rank = 4, 2, 64, 256, 16
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
+    width = (heads + 2 * kv) * dim
+    return PagedAttentionBlock(bf(width, hidden), bf(hidden, heads * dim), heads, kv, dim, requests, 16, 16, 4,
+                               (bf(2, rank, hidden), bf(2, width, rank), None), norm=(None, 1e-5))
+
+
+def test_prompts_buffers_of_an_attention_block_are_recorded_on_every_stream_that_uses_them(streams):
+    block = attention()
+    names = ("slots", "rows", "qkv", "normed", "lora_ws")
+    old = [block._buffers(9)[n] for n in names]
+    for streams.now in (2, 3):
+        assert [block._buffers(9)[n].data_ptr() for n in names] == [t.data_ptr() for t in old]
+    grown = block._buffers(3000)
+    assert {2, 3} <= streams.on(old)
+    assert grown["qkv"].data_ptr() != old[2].data_ptr()
+    assert 3 in streams.on([grown[n] for n in names])
+
+
+def test_step_buffers_of_an_attention_block_are_recorded_too(streams):
+    block = attention()
+    for streams.now in (4, 5):
+        own = block._buffers(4)
+    assert {4, 5} <= streams.on([own[n] for n in ("slots", "rows", "qkv", "normed")])
