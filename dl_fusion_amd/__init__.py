@@ -592,16 +592,33 @@ def _refuse_strided(t, dtype, shape, stride, name):
         raise ValueError(f"{name} must be [{rows}][{cols}] with rows {stride} elements apart")
 
 
-def _stream_of(stream, x, y):
-    """The stream's handle.  A call on the current stream is the current device's: x and y, the first input and the output,
-    have to lie there, since a kernel would fault on another's memory."""
-    if stream is not None:
-        return _stream(stream)
-    here = torch.cuda.current_device()
-    for t in (x, y):
-        if t.__class__ is not int and t is not None and t.get_device() != here:
-            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{here}")
-    return torch._C._cuda_getCurrentRawStream(here)
+def _handle(stream, names, *tensors):
+    """The stream's handle.  All tensors have to be on its device, the current one's where it is None: a kernel would fault
+    on the host's or another device's memory.  A raw handle does not say whose it is: the first tensor's device.  0.5 us for
+    six tensors."""
+    at = -2                     # no device's: the host is -1
+    for t in tensors:
+        if t is not None and t.__class__ is not int:
+            on = t.get_device()
+            if on != at:
+                if on < 0 or at >= 0:
+                    _refuse_device(names, tensors, at)
+                at = on
+    if stream is None:
+        here = torch._C._cuda_getDevice() if at >= 0 else torch.cuda.current_device()
+    elif stream.__class__ is int:
+        return stream
+    else:
+        here = stream.device.index
+    if at >= 0 and at != here:
+        _refuse_device(names, tensors, here)
+    return torch._C._cuda_getCurrentRawStream(here) if stream is None else stream.cuda_stream
+
+
+def _refuse_device(names, tensors, here):
+    for name, t in zip(names, tensors):
+        if t is not None and t.__class__ is not int and (t.get_device() < 0 or t.get_device() != here):
+            raise ValueError(f"{name} is on {t.device}, the call runs on " + (f"cuda:{here}" if here >= 0 else "a GPU"))
 
 
 def _scales(t, rows, stride, name):
@@ -624,7 +641,8 @@ def dlf_rms_norm(desc, x, residual, weight, sum, y, y_scale, stream=None):
                              sum if sum is None else _strided(sum, dtype, shape, desc.sum_stride, "sum"),
                              _strided(y, _TYPES.get(desc.out_dtype), shape, desc.y_stride, "y"),
                              y_scale if y_scale is None else _scales(y_scale, n, desc.scale_stride, "y_scale"),
-                             _stream_of(stream, x, y)), "dlf_rms_norm")
+                             _handle(stream, ("x", "residual", "weight", "sum", "y", "y_scale"), x, residual, weight, sum, y,
+                                     y_scale)), "dlf_rms_norm")
 
 
 def dlf_quant_blocks(desc, x, codes, scale, stream=None):
@@ -632,14 +650,17 @@ def dlf_quant_blocks(desc, x, codes, scale, stream=None):
     shape = desc.rows, desc.cols
     _check(_lib.dlf_quant_blocks(ctypes.byref(desc), _strided(x, _TYPES.get(desc.dtype), shape, desc.x_stride, "x"),
                                  _strided(codes, _FP8, shape, desc.codes_stride, "codes"),
-                                 _scales(scale, shape[0], desc.scale_stride, "scale"), _stream_of(stream, x, codes)),
-           "dlf_quant_blocks")
+                                 _scales(scale, shape[0], desc.scale_stride, "scale"),
+                                 _handle(stream, ("x", "codes", "scale"), x, codes, scale)), "dlf_quant_blocks")
 
 
 def dlf_gemm_blocks_workspace_bytes(desc):
     n = ctypes.c_size_t(0)
     _check(_lib.dlf_gemm_blocks_workspace_bytes(ctypes.byref(desc), ctypes.byref(n)), "dlf_gemm_blocks_workspace_bytes")
     return n.value
+
+
+_GEMM_BLOCKS = ("a", "a_scale", "b", "b_scale", "col_shift", "c", "workspace", "residual")
 
 
 def dlf_gemm_blocks(desc, a, a_scale, b, b_scale, col_shift, residual, c, workspace, workspace_bytes, stream=None):
@@ -654,7 +675,8 @@ def dlf_gemm_blocks(desc, a, a_scale, b, b_scale, col_shift, residual, c, worksp
                                 col_shift if col_shift is None else _scales(col_shift, 1, n, "col_shift"),
                                 residual if residual is None else _strided(residual, _BF16, shape, n, "residual"),
                                 _strided(c, _BF16, shape, n, "c"), _workspace(workspace, workspace_bytes),
-                                workspace_bytes, _stream_of(stream, a, c)), "dlf_gemm_blocks")
+                                workspace_bytes, _handle(stream, _GEMM_BLOCKS, a, a_scale, b, b_scale, col_shift, c,
+                                                         workspace if workspace_bytes else None, residual)), "dlf_gemm_blocks")
 
 
 def dlf_gemm_blocks_gated(desc, a, a_scale, b, b_scale, col_shift, gate, c, workspace, workspace_bytes, stream=None):
@@ -667,7 +689,9 @@ def dlf_gemm_blocks_gated(desc, a, a_scale, b, b_scale, col_shift, gate, c, work
                                       _scales(b_scale, 2 * -(-n // 256), desc.b_scale_stride, "b_scale"),
                                       col_shift if col_shift is None else _scales(col_shift, 1, n, "col_shift"),
                                       GATES.get(gate, gate), _strided(c, _BF16, (m, n // 2), n // 2, "c"),
-                                      _workspace(workspace, workspace_bytes), workspace_bytes, _stream_of(stream, a, c)),
+                                      _workspace(workspace, workspace_bytes), workspace_bytes,
+                                      _handle(stream, _GEMM_BLOCKS, a, a_scale, b, b_scale, col_shift, c,
+                                              workspace if workspace_bytes else None)),
            "dlf_gemm_blocks_gated")
 
 
