@@ -64,6 +64,10 @@ class GatedFeedForward:
         _packed(down, self.d_model, self.d_ff, -(-self.d_model // 128), "down")
         if norm is not None and (tuple(norm.shape) != (self.d_model,) or norm.dtype != torch.float32):
             raise ValueError(f"norm must be fp32 [{self.d_model}]")
+        device = down[0].device
+        for t, name in ((gate_up[0], "gate and up codes"), (gate_up[1], "gate and up scales"), (down[1], "down scales"), (norm, "norm")):
+            if t is not None and t.device != device:
+                raise ValueError(f"{name} are on {t.device}, the down codes on {device}")
         self.rows = rows
         self._own_room = self._allocate(rows) if rows > 0 else None
         self._own = self._views(rows, self._own_room) if rows > 0 else None

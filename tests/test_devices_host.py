@@ -103,3 +103,16 @@ def test_all_tensors_on_another_device_than_the_stream_s(library, call):
             call(stream, there)
     with pytest.raises(Reached):            # a handle may be any device's
         call(0, there)
+
+
+@pytest.mark.parametrize("part", ["gate and up codes", "gate and up scales", "down scales", "norm"])
+def test_a_feed_forward_block_s_weights_are_on_one_device(part):
+    from dl_fusion_amd.feed_forward import GatedFeedForward, pack, pack_gate_up
+    w = torch.ones(32, 16).numpy()
+    gate_up, down, norm = pack_gate_up(w, w, "cpu"), pack(w.T.copy(), "cpu"), torch.ones(16)
+    GatedFeedForward(gate_up, down, norm)
+    off = lambda t: t.to("meta")  # noqa: E731
+    bad = {"gate and up codes": dict(gate_up=(off(gate_up[0]), gate_up[1])), "gate and up scales": dict(gate_up=(gate_up[0], off(gate_up[1]))),
+           "down scales": dict(down=(down[0], off(down[1]))), "norm": dict(norm=off(norm))}[part]
+    with pytest.raises(ValueError, match=part):
+        GatedFeedForward(**{**dict(gate_up=gate_up, down=down, norm=norm), **bad})
