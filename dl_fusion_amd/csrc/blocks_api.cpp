@@ -125,6 +125,7 @@ extern "C" dlf_status dlf_rms_norm(const dlf_rms_norm_desc* d, const void* x, co
     a.scale_stride = d->scale_stride;
     a.eps = d->eps;
     a.inv_scale = d->out_inv_scale;
+    a.inv_cols = 1.0 / d->cols;
     const int out = d->out_dtype == DLF_F32 ? dlf::kOutF32 : d->out_dtype == DLF_BF16 ? dlf::kOutBf16 : dlf::kOutFp8;
     return hip_status(dlf::launch_rms_norm(a, d->dtype == DLF_F32, out, static_cast<hipStream_t>(stream)), "dlf_rms_norm");
 }

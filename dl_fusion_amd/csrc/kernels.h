@@ -254,6 +254,7 @@ struct RmsNormArgs {
     int64_t x_stride, residual_stride, sum_stride, y_stride;
     int cols, scale_stride;
     float eps, inv_scale;
+    double inv_cols;            // 1 / cols
 };
 // out: kOutBf16 / kOutF32 / kOutFp8 (block scales where scale is given, else inv_scale)
 hipError_t launch_rms_norm(const RmsNormArgs& args, bool f32, int out, hipStream_t stream);

@@ -424,7 +424,8 @@ typedef struct {
  *     h   = x [+ residual]
  *     sum = h, rounded once
  *     y   = h / sqrt(mean(h^2) + eps) * weight
- * in fp32, y from h as it was before sum's rounding, and rounded once: to bf16,
+ * in fp32 (1 / sqrt(..) in 64 bits, rounded once), y from h as it was before sum's
+ * rounding, and rounded once: to bf16,
  * to e4m3 by a static scale, Q(fp32(y * out_inv_scale)), for dlf_gemm_fused, or,
  * with y_scale, to codes and block scales, for dlf_gemm_blocks (a NaN stays a NaN
  * in both).  A row whose sum of squares passes fp32's range is summed again 2^-80

@@ -1,0 +1,38 @@
+"""How often the root-mean-square norm rounds, on rows whose sums of squares are exact: whole numbers, at most 2^24 in all.
+
+With u = 2^-24: the mean and eps are added in 64 bits, their root's reciprocal is rounded to fp32 once (u of it, and less than
+2^-40 from 64 bits), and so is the product by a value (u), none where the value is a power of two.  Bounds, derived before any
+run: u (1 + 2^-10) for those, 2 u (1 + 2^-10) for all."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+U = 2.0 ** -24 * (1 + 2.0 ** -10)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    torch.cuda.set_device(0)
+
+
+@pytest.mark.parametrize("eps", [2.0 ** -100, 1e-5, 0.375])
+@pytest.mark.parametrize("rows,cols", [(4000, 5), (4000, 64), (3000, 1000), (2000, 2048), (1000, 4100), (300, 9000), (100, 20000)])
+def test_the_root_and_its_reciprocal_are_rounded_once(rows, cols, eps):
+    import dl_fusion_amd as dl
+    g = torch.Generator().manual_seed(cols)
+    x = torch.randint(-9, 10, (rows, cols), generator=g).float() * torch.randint(0, 2, (rows, 1), generator=g).mul(2).add(1)
+    x[:, 0] = 1
+    x = x.cuda()
+    y = torch.empty_like(x)
+    d = dl.rms_norm_desc(rows, cols, eps, "f32", "f32")
+    dl.dlf_rms_norm(d, x, None, None, None, y, None)
+    v = x.double()
+    want = v / (v.square().mean(1, keepdim=True) + d.eps).sqrt()
+    off = (y - want).abs()
+    power = v.abs().log2().frac() == 0
+    assert power[:, 0].all()
+    assert (off <= U * want.abs())[power].all()
+    assert (off <= 2 * U * want.abs()).all()
