@@ -17,6 +17,7 @@ class Streams:
         monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: self.capturing)
         monkeypatch.setattr(torch.cuda, "current_stream", lambda *_: self.now)
         monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda _: self.now, raising=False)
+        monkeypatch.setattr(torch.Tensor, "is_cuda", True)
         monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: self.seen.setdefault(t.data_ptr(), set()).add(s))
 
     def on(self, tensors):
