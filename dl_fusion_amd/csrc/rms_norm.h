@@ -241,15 +241,16 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR, V == 1 ? 8 : 4) void rms_nor
             }
         }
         float total = squares(1.0f);
-        float factor = 1.0f, eps = p.eps;
+        float factor = 1.0f;
+        double eps = p.eps;
         if (__builtin_expect(total == INFINITY, 0)) {
-            // past fp32's range, or an infinity among them: the row 2^-80 times as large (2^23 squares of 2^48
-            // fit), where eps is nothing beside it; h * r itself would need an r below the normal numbers
+            // past fp32's range, or an infinity among them: the row, and eps with it, 2^-80 times as large (2^23 squares of
+            // 2^48 fit); h * r itself would need an r below the normal numbers
             factor = 0x1p-80f;
-            eps = 0.0f;
+            eps *= 0x1p-160;
             total = squares(factor);
         }
-        const float r = rsqrt_once(static_cast<double>(total) * p.inv_cols + static_cast<double>(eps));
+        const float r = rsqrt_once(static_cast<double>(total) * p.inv_cols + eps);
         auto finish = [&](int at, int j, const float* v) __attribute__((always_inline)) {
             const int n = cols - at;
             float y[8];

@@ -36,3 +36,20 @@ def test_the_root_and_its_reciprocal_are_rounded_once(rows, cols, eps):
     assert power[:, 0].all()
     assert (off <= U * want.abs())[power].all()
     assert (off <= 2 * U * want.abs()).all()
+
+
+@pytest.mark.parametrize("cols", [1, 6, 40, 520, 4096, 20000])
+@pytest.mark.parametrize("eps", [1e30, 1e37, 3e38])
+def test_an_eps_beside_squares_past_the_range(cols, eps):
+    """Rows of sums up to and past fp32's range, and an eps that counts beside their mean.  A sum is a chain of at most cols / 64
+    + 40 additions, which the root halves; 3 u for its rounding, the product and the squares."""
+    import dl_fusion_amd as dl
+    g = torch.Generator().manual_seed(cols)
+    x = (torch.rand(12, cols, generator=g) + 1) * torch.logspace(14, 20, 12)[:, None]
+    x = x.cuda()
+    y = torch.empty_like(x)
+    d = dl.rms_norm_desc(12, cols, eps, "f32", "f32")
+    dl.dlf_rms_norm(d, x, None, None, None, y, None)
+    v = x.double()
+    want = v / (v.square().mean(1, keepdim=True) + d.eps).sqrt()
+    assert ((y - want).abs() <= ((cols / 64 + 40) / 2 + 3) * U * want).all(), (y / want - 1).abs().max(1).values.tolist()
