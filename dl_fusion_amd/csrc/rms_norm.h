@@ -213,22 +213,26 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR, V == 1 ? 8 : 4) void rms_nor
         Raw8<float> early[kEarly ? V : 1];
         float h[V > 0 ? V : 1][8];
         auto squares = [&](float factor) __attribute__((always_inline)) {
-            float s = 0.0f;
-            auto add = [&](const float* v) __attribute__((always_inline)) {
+            auto add = [&](float s, const float* v) __attribute__((always_inline)) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const float u = v[i] * factor;
                     s = fmaf(u, u, s);
                 }
+                return s;
             };
+            float s = 0.0f;
             if constexpr (V > 0) {
 #pragma unroll
-                for (int j = 0; j < V; ++j) add(h[j]);
+                for (int j = 0; j < V; ++j) s = add(s, h[j]);
             } else {
+                // thousands of values a thread: chunks are added in 64 bits (in fp32 alone, 2^23 columns of 1.1 were off by 470 2^-24)
+                double all = 0.0;
                 for (int at = 8 * tid; at < cols; at += 8 * TPR) {
                     load_h(at, h[0]);
-                    add(h[0]);
+                    all += static_cast<double>(add(0.0f, h[0]));
                 }
+                s = static_cast<float>(all);
             }
             return all_sum(s);
         };

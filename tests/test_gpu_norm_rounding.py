@@ -53,3 +53,20 @@ def test_an_eps_beside_squares_past_the_range(cols, eps):
     v = x.double()
     want = v / (v.square().mean(1, keepdim=True) + d.eps).sqrt()
     assert ((y - want).abs() <= ((cols / 64 + 40) / 2 + 3) * U * want).all(), (y / want - 1).abs().max(1).values.tolist()
+
+
+@pytest.mark.parametrize("cols", [16392, 131080, (1 << 20) + 5, 1 << 23])
+@pytest.mark.parametrize("value", [1.1, 0.7, 1e16])
+def test_rows_of_one_value_however_long(cols, value):
+    """Sums that round the same way again and again.  A chunk of 8 squares is off by 8 u at most, a thread's sum of chunks
+    by u, the joins of 64 lanes and 16 waves by 22 u, the root halves it; 3 u for its rounding and the product.  (1e16: the longest
+    rows pass fp32's range, and are taken 2^-80 times as large, which is exact.)"""
+    import dl_fusion_amd as dl
+    x = torch.full((2, cols), value, device="cuda")
+    y = torch.empty_like(x)
+    d = dl.rms_norm_desc(2, cols, 1e-5, "f32", "f32")
+    dl.dlf_rms_norm(d, x, None, None, None, y, None)
+    v = float(x[0, 0])
+    want = v / (v * v + d.eps) ** 0.5
+    off = float((y.double() - want).abs().max()) / want
+    assert off <= (31 / 2 + 3) * U, off * 2 ** 24
