@@ -4,8 +4,8 @@
 //     c = act(acc + shift [+ residual]),  or gate(acc[2j]) * acc[2j + 1]
 //
 // v_mfma_f32_16x16x128_f8f6f4 sums just one block: its result, from a zero start, is scaled and added to
-// the fp32 sum by one FMA a value.  (Inside a block it aligns the products to the largest of a group and cuts what lies
-// 2^-14 below that: measured 2e-6 rms of sum |a b| on normal values.  The 16x16x32 form does the same; exact
+// the fp32 sum by one FMA a value.  (Inside a block it aligns the products to the largest of a group of 8 and cuts
+// what lies 2^-14 below that: measured 2e-6 rms of sum |a b| on normal values.  The 16x16x32 form does the same; exact
 // sums would take the bf16 forms at half the rate, and c has 2^-9 of its own.)
 #pragma once
 

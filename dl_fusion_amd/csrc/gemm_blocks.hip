@@ -101,7 +101,8 @@ __global__ __launch_bounds__(T::NT, T::kWaves) void gemm_blocks_kernel(const Gem
         return static_cast<int>(at) + 16 * chunk < k ? from + at : kOutOfRange;
     };
     // Load q of this wave's of a block, whose offset is `off`, to a stage: b's, then those of a's with the first halves of the
-    // waves' rows, which are wanted first, then the second halves'.  Past the last block and past k: zeros.
+    // waves' rows, which are wanted first, then the second halves'.  Past k: zeros.  Past the end of a part of the sum: the next
+    // part's blocks, STAGES of them, which nobody reads.
     auto load_part = [&](int stage, int q, uint32_t off) {
         uint8_t* const to = lds + stage + wave * 1024;
         if (q < T::LB) {

@@ -131,3 +131,25 @@ def test_values_that_are_not_finite(kind, parts):
     s["a"].view(torch.uint8)[m - 1, k - 1], s["b"].view(torch.uint8)[7, 130] = codes
     s["a_scale"][1, 0], s["b_scale"][1, 3] = keep
     assert within(product(s), want, off).all()
+
+
+@pytest.mark.parametrize("m", [1, 64, 1057])
+@pytest.mark.parametrize("small", [1.0, 2.0, 3.25, 3.5, 5.0, 9.0, 13.0, 30.0, "positive", "normal"])
+def test_what_an_outlier_takes_from_its_neighbours(m, small):
+    """One product of 448 x 448, 2^17 at its power of two, among 127 others: 7 neighbours lose less than 2^-14 of that each.  The
+    shift takes the large product away again, so that the others' sum is seen; fp32 sums of 2^18 round by 2^-6 at most."""
+    import dl_fusion_amd as dl
+    n, k = (64, 128) if m < 1000 else (7376, 128)
+    g = torch.Generator().manual_seed(5)
+    draw = {"positive": lambda: torch.rand(k, generator=g) * 3, "normal": lambda: torch.randn(k, generator=g) * 3}
+    a, b = (draw[small]() if small in draw else torch.full((k,), small) for _ in range(2))
+    a[0] = b[0] = 448.0
+    a, b = a.to(torch.float8_e4m3fn), b.to(torch.float8_e4m3fn)
+    want = float((a.double() * b.double())[1:].sum())
+    sa, sb = torch.ones(m, 4, device="cuda"), torch.ones(-(-n // 128), 4, device="cuda")
+    c = torch.empty(m, n, dtype=torch.bfloat16, device="cuda")
+    shift = torch.full((n,), -448.0 * 448.0, device="cuda")
+    d = dl.gemm_blocks_desc(m, n, k)
+    assert dl.dlf_gemm_blocks_workspace_bytes(d) == 0
+    dl.dlf_gemm_blocks(d, a.repeat(m, 1).cuda(), sa, b.repeat(n, 1).cuda(), sb, shift, None, c, None, 0)
+    assert ((c.double() - want).abs() <= 7 * 2.0 ** -14 * 2 ** 17 + 2.0 ** -6 + 2.0 ** -9 * c.double().abs()).all(), (float(c[0, 0]), want)
