@@ -8,10 +8,12 @@
 // is read in whole lines and 16 neighbouring lanes hold a block of 128 columns: its largest magnitude is a
 // maximum over those lanes, no LDS.
 //
-// On the device, from a graph: 8192 rows of 4096 bf16 columns with residual and sum into codes 42 us (5.6 TB/s; a copy
-// reaches 5.2), 64 rows 3.3 us, one row into bf16 2.6 us, against 2.2 us of an empty kernel; the quantiser 8192 rows of 4096
-// columns 20 us (5.0 TB/s), 64 rows 2.3.  Rows that do not start at 16 bytes cost up to a quarter more (8192 x 4096, us: stride
-// 4096 | 4097, bf16 output 45.8 | 55.2, codes 41.8 | 48.3; 4095 columns close together 57.4 and 51.2; fp32 rows nothing).
+// On the device, from a graph: 8192 rows of 4096 bf16 columns with residual and sum into codes 42 to 44 us (5.4 to 5.6 TB/s; a copy
+// reaches 5.2), 64 rows 3.3 to 3.5 us, one row into bf16 2.6 to 2.9 us, against 2.2 us of an empty kernel; the quantiser 8192 rows of
+// 4096 columns 20 us (5.0 TB/s), 64 rows 2.3.  Rows that do not start at 16 bytes cost up to a quarter more (8192 x 4096, us: stride
+// 4096 | 4097, bf16 output 45 | 57, codes 44 | 51; 4095 columns close together 61 and 56; fp32 rows nothing).  Two kinds of rows are
+// far from their bytes: short ones, a wave each however few lanes they fill (262144 x 128 without residual 75 us, 26 of bytes), and
+// those above 16384 columns, which are read twice (1024 x 20000 with residual and sum 43 us, 32 of bytes).
 #pragma once
 
 #include "block_scale.h"
